@@ -49,7 +49,9 @@ typedef enum {
   LB_ERR_CUDA = 4,        /* a CUDA runtime call failed (see littlebit_last_cuda_error) */
   LB_ERR_TIMEOUT = 5,     /* a bounded device wait ran out (littlebit_device_status) */
   LB_ERR_UNSUPPORTED = 6, /* a valid request this build does not implement */
-  LB_ERR_RANGE = 7        /* a value left the range of the format it is held in (littlebit_device_status) */
+  LB_ERR_RANGE = 7,       /* a value left the range of the format it is held in (littlebit_device_status) */
+  LB_ERR_PAGES = 8,       /* a paged cache had no free page, or a slot no room, for what was asked (littlebit_device_status) */
+  LB_ERR_INDEX = 9        /* an index in device memory lay outside its cache, or a slot was not free (littlebit_device_status) */
 } lb_status;
 
 typedef enum { LB_F16 = 0, LB_BF16 = 1, LB_F32 = 2, LB_I8 = 3 } lb_dtype;
@@ -326,6 +328,211 @@ lb_status littlebit_linear_forward_noalloc(const lb_layer* layer, const void* x_
                                            int batch, lb_dtype xdt, void* stream);
 
 /*
+ * The paged cache: rows of many sequences in pages, and the operators of a
+ * serving step around them -- rotary positions, rows written to and read from
+ * pages, page bookkeeping, and attention.  (The pages of the method describe
+ * the latent rows that such a cache may hold, Samsung LittleBit article,
+ * section 4, the KV-cache bullet; these operators have no counterpart in them.)
+ *
+ * A cache has n_pages pages of page_size rows (a power of two, 8..1024).  A
+ * plane holds one row of `heads` x `width` values per cached token: K or V of
+ * one layer, or a layer's latent rows (heads = 1, width =
+ * littlebit_latent_row_elems).  Element (page, head, row, c) of a plane is at
+ * data[page * stride_page + head * stride_head + row * stride_row + c]
+ * (strides in elements, any order).  All planes share the page numbers.
+ *   table  [n_slots][table_stride]  pages of each sequence slot, in order;
+ *          max_pages (<= table_stride) entries are used, -1 where none
+ *   length [n_slots]                tokens held by each slot
+ *   refs   [n_pages]                slots that hold the page; 0: free
+ * The arrays are device memory of the caller; an empty cache has table = -1,
+ * length = 0, refs = 0.  Row r of the whole cache is row r % page_size of
+ * page r / page_size; the `where` arrays below hold such numbers.
+ *
+ * Everything the bookkeeping calls decide lies in device memory, so a serving
+ * step of them may be captured into a CUDA graph.  They allocate the
+ * lowest-numbered free pages, in the order of the lists given.  What cannot be
+ * done is left out as a whole (a sequence is not extended, a child not made)
+ * and raises a bit in the cache status word of the device, which
+ * littlebit_device_status returns: LB_ERR_PAGES, no free page or no room in
+ * max_pages; LB_ERR_INDEX, a slot, page or row number outside the cache, a
+ * slot twice in one list, a fork into a slot that holds tokens.  A slot number
+ * of -1 in a list is padding and skipped.  Lists take up to 4096 entries.
+ * Calls that change one cache must be ordered by the caller.  Alignment: every
+ * plane's and row tensor's base on 16 bytes, strides and row sizes multiples
+ * of 16 bytes.  None of these calls allocates device memory.
+ */
+typedef struct lb_plane {
+  void* data;
+  int64_t stride_page, stride_head, stride_row;   /* elements */
+  int heads, width;
+  lb_dtype dt;
+} lb_plane;
+
+typedef struct lb_cache {
+  const lb_plane* planes;   /* host array, 1..1024 planes */
+  int n_planes;
+  int n_pages, page_size, n_slots, max_pages;
+  int64_t table_stride;
+  int32_t* table;
+  int32_t* length;
+  int32_t* refs;
+} lb_cache;
+
+/* Rows of tokens: element (t, head, c) at data[t * stride_token + head * stride_head + c] (strides in elements). */
+typedef struct lb_rows {
+  void* data;
+  int64_t stride_token, stride_head;
+  int heads, width;
+} lb_rows;
+
+/*
+ * Rotary positions.  Pair i of a head (i < rotary_dim / 2) is turned by the
+ * angle pos * f_i, f_i = base^(-2i / rotary_dim) radians per token:
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin),
+ * with (a, b) at elements (i, i + rotary_dim/2), or (2i, 2i + 1) if
+ * `interleaved`; elements from rotary_dim on are left alone.  inverse = 1
+ * turns back (with scale 1 the transposed rotation, hence also the gradient).
+ * phases holds f_i / 2 pi as 64-bit fractions of a turn, so that pos * phase
+ * modulo 2^64 is the angle, without loss at any position.
+ */
+typedef struct lb_rotary {
+  const uint64_t* phases;   /* device, rotary_dim / 2 */
+  int rotary_dim;           /* multiple of 16, at most the width of the rows */
+  int interleaved;
+  float scale;
+} lb_rotary;
+
+/*
+ * Host: the phases of f_i, stretched for a context `factor` times as long.
+ * original = 0: every f_i is divided by factor.  original > 0: a pair that
+ * makes turns = original * f_i / 2 pi turns over the original context keeps
+ * f_i where turns >= fast, gets f_i / factor where turns <= slow, and in
+ * between the mix keep * f_i + (1 - keep) * f_i / factor, keep = (turns - slow)
+ * / (fast - slow), or with log_ramp = 1 the same ramp in log(turns).
+ * Errors: LB_ERR_ARG (null, base or factor not positive, fast <= slow with
+ * original > 0, slow <= 0 with log_ramp), LB_ERR_SHAPE (rotary_dim not a
+ * positive even number).
+ */
+lb_status littlebit_rotary_phases(int rotary_dim, double base, double factor, double original, double slow,
+                                  double fast, int log_ramp, uint64_t* phases_host);
+
+/*
+ * Rotates n tensors (1..8) of n_tokens rows of one dtype (LB_F16, LB_BF16,
+ * LB_F32) in one launch: dst[i] = rotated src[i]; dst[i].data may be
+ * src[i].data with the same strides.  positions_dev: int32 per token, any sign.
+ * Angles are exact, cos and sin fp32, one rounding to the dtype.
+ * Errors: LB_ERR_ARG, LB_ERR_SHAPE, LB_ERR_ALIGN, LB_ERR_CUDA.
+ */
+lb_status littlebit_rotary(const lb_rows* src, const lb_rows* dst, int n, int n_tokens, lb_dtype dt,
+                           const int32_t* positions_dev, const lb_rotary* rope, int inverse, void* stream);
+
+/*
+ * Makes room for new tokens: sequence i of the list (slot slots_dev[i]) grows
+ * by starts_dev[i + 1] - starts_dev[i] tokens, the tokens starts[i] ..
+ * starts[i + 1] - 1 of the step (starts: n + 1 ascending int32).  Pages are
+ * taken, table, length and refs updated, and for each of the n_tokens tokens
+ *   where_dev[t]     <- its row in the cache (int64), -1 if it has none
+ *   positions_dev[t] <- its index in its sequence, plus the length of slot
+ *                       `prefix` if that is >= 0 (-1 with where = -1)
+ * One launch.  A sequence whose last page is shared must not grow (forks own
+ * their last, partly filled page, so extending a fork never meets one).
+ */
+lb_status littlebit_cache_extend(const lb_cache* c, const int32_t* slots_dev, const int32_t* starts_dev, int n,
+                                 int n_tokens, int prefix, int64_t* where_dev, int32_t* positions_dev, void* stream);
+
+/*
+ * where and positions, as above, of tokens that the cache holds: the tokens
+ * starts[i] .. starts[i + 1] - 1 are tokens first_dev[i], first_dev[i] + 1, ...
+ * of slot slots[i] (first_dev null: from the slot's first token on).
+ */
+lb_status littlebit_cache_locate(const lb_cache* c, const int32_t* slots_dev, const int32_t* starts_dev,
+                                 const int32_t* first_dev, int n, int n_tokens, int prefix, int64_t* where_dev,
+                                 int32_t* positions_dev, void* stream);
+
+/*
+ * Writes the rows of n_tokens tokens into n planes (1..7, host list of plane
+ * numbers): rows[i] goes to plane planes[i] at row where_dev[t]; a token with
+ * where -1 is skipped.  Planes whose bit i is set in `rotated` get the rows
+ * rotated (rope, positions_dev).  q, if not null, is rotated into q_out by the
+ * same launch (every token, also skipped ones).  All of one dtype, that of the
+ * planes: LB_F16, LB_BF16 or LB_F32.  One launch.
+ */
+lb_status littlebit_cache_write(const lb_cache* c, const int* planes, const lb_rows* rows, int n, int n_tokens,
+                                const int64_t* where_dev, const lb_rotary* rope, const int32_t* positions_dev,
+                                unsigned int rotated, const lb_rows* q, const lb_rows* q_out, void* stream);
+
+/* The other way: rows[i] <- the rows where_dev[t] of plane planes[i]; rows of
+ * tokens with where -1 are left as they were.  E.g. latent rows for
+ * littlebit_latent_expand. */
+lb_status littlebit_cache_read(const lb_cache* c, const int* planes, const lb_rows* rows, int n, int n_tokens,
+                               const int64_t* where_dev, void* stream);
+
+/*
+ * Slot children[i] becomes a copy of slot parents[i]: it shares the parent's
+ * full pages (refs + 1) and gets a page of its own for a partly filled last
+ * one, into which the rows held are copied, in every plane.  Children must be
+ * empty.  A parent may be named many times.  work_dev:
+ * littlebit_cache_fork_work(n) bytes, 16-byte aligned.  Two launches (one more
+ * for every further 64 planes).
+ */
+size_t littlebit_cache_fork_work(int n);
+lb_status littlebit_cache_fork(const lb_cache* c, const int32_t* parents_dev, const int32_t* children_dev, int n,
+                               void* work_dev, void* stream);
+
+/* Empties the slots: their pages lose a reference, their table rows become -1.
+ * Empty slots, and a slot named twice, are fine.  One launch. */
+lb_status littlebit_cache_free(const lb_cache* c, const int32_t* slots_dev, int n, void* stream);
+
+/*
+ * Moves the pages in use to the lowest numbers: with L pages in use, the k-th
+ * one at or above L moves to the k-th free one below L, in every plane, and
+ * table and refs follow.  The new tables go to table_out (strided as table)
+ * and refs_out, which may be the cache's own arrays; otherwise those, and the
+ * rows they lead to, stay good for work under way until a page is taken
+ * again.  count_dev <- L.  work_dev: littlebit_cache_compact_work(n_pages)
+ * bytes, 16-byte aligned.  Two launches (as littlebit_cache_fork).
+ */
+size_t littlebit_cache_compact_work(int n_pages);
+lb_status littlebit_cache_compact(const lb_cache* c, int32_t* table_out, int32_t* refs_out, int32_t* count_dev,
+                                  void* work_dev, void* stream);
+
+/* Copies page src_dev[i] to page dst_dev[i] in every plane, i < n (n up to
+ * 2^20).  No page may be both a source and a destination of one call, or a
+ * destination twice.  Tables are not touched. */
+lb_status littlebit_cache_copy(const lb_cache* c, const int32_t* src_dev, const int32_t* dst_dev, int n,
+                               void* stream);
+
+/*
+ * Attention of new tokens over the cache, for a batch whose sequences share a
+ * prefix:
+ *   out[t, h] = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q[t, h] . k_j)
+ * over the tokens j of slot `prefix` (all of them; none if prefix is -1) and
+ * the tokens of t's own slot up to t itself.  Sequence i of the list has the
+ * tokens starts[i] .. starts[i + 1] - 1 of q, which are the last tokens of
+ * slot slots[i]; rows of q in no sequence are left out and their rows of out
+ * left as they were.  A token that sees nothing (prefix and slot empty) gets
+ * zeros.  K is plane k, V plane v (fp16 or bf16, equal shape, width 64 or
+ * 128); q and out have their dtype, q.heads a multiple of the planes' heads:
+ * query head h reads head h / (q.heads / heads).  most_q: a bound on the
+ * tokens of any one sequence; tokens past it are cut off.
+ * The prefix is read and multiplied once for the whole batch.  Scores, sums
+ * and outputs are accumulated in fp32; the weights are rounded to the dtype
+ * for the product with V, the outputs once at the end.  Rows past a
+ * sequence's end are never used, whatever they hold.  (A non-finite V of a
+ * token may reach the outputs of earlier tokens of the same call and
+ * sequence, whose weight for it is zero.)
+ * work_dev: littlebit_cache_attend_work bytes, 256-byte aligned, needed until
+ * the call's launches are done; calls that may overlap need their own.
+ * Errors: LB_ERR_ARG, LB_ERR_SHAPE, LB_ERR_ALIGN, LB_ERR_UNSUPPORTED (dtype
+ * or width), LB_ERR_CUDA.
+ */
+size_t littlebit_cache_attend_work(const lb_cache* c, int k, int heads_q, int n_tokens, int n, int most_q,
+                                   int with_prefix);
+lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows* q, int n_tokens,
+                                 const int32_t* slots_dev, const int32_t* starts_dev, int n, int prefix, int most_q,
+                                 float scale, const lb_rows* out, void* work_dev, size_t work_bytes, void* stream);
+
+/*
  * (Host helpers below: no counterpart in the pages.)
  * Waits for `stream`, then returns in *status the device-side error bits that
  * the forward kernels enqueued on it have raised since the last call, and
@@ -337,7 +544,9 @@ lb_status littlebit_linear_forward_noalloc(const lb_layer* layer, const void* x_
  * finite range (|x| > 65504; prefill converts x to fp16), or a latent value
  * t' = l (.) t, or an fp16 output y, beyond fp16's range (prefill).
  * The word of littlebit_linear_forward_noalloc on the current device is read
- * and cleared too (its calls may be on any stream: synchronise them first).
+ * and cleared too (its calls may be on any stream: synchronise them first), and
+ * likewise the word of the paged cache's calls on the current device, whose
+ * bits are (1 << LB_ERR_PAGES) and (1 << LB_ERR_INDEX) (see there).
  * *status is 0 when nothing was raised.  Errors: LB_ERR_ARG, LB_ERR_CUDA.
  */
 lb_status littlebit_device_status(void* stream, unsigned int* status);

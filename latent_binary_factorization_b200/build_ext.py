@@ -10,7 +10,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "liblittlebit.so")
-SOURCES = ["littlebit_capi.cu", "pack.cu", "decode.cu", "prefill.cu", "init.cu", "noalloc.cu", "selfcheck.cu"]
+SOURCES = ["littlebit_capi.cu", "pack.cu", "decode.cu", "prefill.cu", "init.cu", "noalloc.cu", "selfcheck.cu", "cache.cu",
+           "attend.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -244,6 +244,15 @@ size_t path_scratch_bytes(const lb_layer& L, int batch);
 // device `dev`, or null before that entry point's first call on the device.
 unsigned int* noalloc_status_word(int dev);
 
+// cache.cu: argument checks shared with attend.cu, and the status word of the
+// paged cache's calls (null before the first of them on the device).
+lb_status check_cache(const lb_cache* c);
+lb_status check_list(const lb_cache* c, const void* slots, const void* starts, int n, int n_tokens, int prefix);
+lb_status check_cache_plane(const lb_cache* c, int i);
+lb_status check_token_rows(const lb_rows* r, lb_dtype dt);
+unsigned int* cache_status_word(int dev);
+cudaError_t touch_cache_status(unsigned int** word);
+
 // init.cu: Dual-SVID and Joint-ITQ (scratch sizes in floats)
 size_t dual_svid_scratch_floats(int d_out, int d_in, int s);
 cudaError_t launch_dual_svid(const float* Uf, const float* Vf, int d_out, int d_in, int s, int iters, void* U_bits,

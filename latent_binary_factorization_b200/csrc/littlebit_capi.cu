@@ -797,9 +797,9 @@ lb_status littlebit_device_status(void* stream, unsigned int* status) {
     }
     *status |= bits;
   }
-  // the allocation-free forward's word on this device (any stream)
-  unsigned int* word = lb::noalloc_status_word(dev);
-  if (word) {
+  // the words of the allocation-free forward and of the paged cache on this device (any stream)
+  for (unsigned int* word : {lb::noalloc_status_word(dev), lb::cache_status_word(dev)}) {
+    if (!word) continue;
     unsigned int bits = 0;
     e = cudaMemcpy(&bits, word, sizeof(bits), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -952,6 +952,8 @@ const char* littlebit_status_string(lb_status st) {
     case LB_ERR_TIMEOUT: return "LB_ERR_TIMEOUT: device wait timed out";
     case LB_ERR_UNSUPPORTED: return "LB_ERR_UNSUPPORTED: not implemented for these arguments";
     case LB_ERR_RANGE: return "LB_ERR_RANGE: a value left the range of its format";
+    case LB_ERR_PAGES: return "LB_ERR_PAGES: no free page, or no room in a slot";
+    case LB_ERR_INDEX: return "LB_ERR_INDEX: an index outside its cache, or a slot in use";
   }
   return "unknown lb_status";
 }
