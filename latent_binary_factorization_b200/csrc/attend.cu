@@ -19,12 +19,14 @@
 // partials in the order of their blocks: the result does not depend on timing.
 // The lengths are read on the device, so a captured graph follows a growing
 // cache.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "lb_internal.h"
 
@@ -558,6 +560,448 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   if (bad) atomicOr(a.status, bad);
 }
 
+// ------------------------------------------------------------------ many rows
+
+// Tiles of 128 or 256 query rows on the tcgen05 tensor cores: for the prefix
+// of a batch, which all of its rows read, and for sequences with many new
+// tokens.
+//
+// A block has two softmax groups of four warps, each with a tile of 128 query
+// rows in shared memory, its scores (fp32, 128 columns; the weights take their
+// place as 16-bit pairs in the first 64) and its output (fp32) in tensor
+// memory: 2 x (128 + 128) columns, all 512.  One warp loads K and V tiles of
+// 128 keys by TMA, page by page, into a ring; one thread issues the products:
+//   S = Q K^T (both from shared memory), O += P V (P from tensor memory, V as
+//   it lies, keys down, i.e. N-major).
+// Each thread of a group owns one row, so the row's maximum and sum need no
+// exchange.  While one group takes its softmax the other's products run: the
+// issue order is PV(v), QK(v + 2) for steps v = 0, 1, ..., step v belonging to
+// group v % 2, and since the tensor core works in that order, S(v + 2) being
+// complete means that PV(v) is: no other barrier guards a group's scores or
+// its output.
+//   WIDE (more than 128 rows): the groups have different rows and share every
+//   K and V tile, which halves what has to come out of L2.
+//   else: the groups have the same rows and take every other key tile; each
+//   leaves a partial of its own (two `ways` a slot).
+// The running maximum is raised, and O rescaled in tensor memory, only when a
+// tile's maximum exceeds it by more than 8 (a factor 256, which the 16-bit
+// weights and fp32 sums hold without loss of precision), i.e. hardly ever after
+// the first tiles.  V rows past the end of the keys are zeroed in shared memory
+// (0 x NaN is not 0), scores there are masked, so K may hold anything.
+constexpr int kTile = 128;         // rows of a group's query tile; keys of a K or V tile
+constexpr int kManyThreads = 384;   // two softmax groups, and one whose first two warps load and multiply
+// The launch's registers, 168 a thread, are shared out again: 2 x 216 + 72 = 3 x 168.
+constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
+template <int D> constexpr int kTileBytes = kTile * D * 2;
+template <int D> constexpr int kRing = D == 128 ? 5 : 10;   // K and V tiles in flight
+template <int D> constexpr int kManySmem = (2 + kRing<D>) * kTileBytes<D> + 1024;
+constexpr float kRaise = 8.f;
+
+__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_addr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_addr(b)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(shared_addr(b)), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+// Bounded: false when the phase has not completed after kSpinLimit polls.
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity) {
+  for (int i = 0; i < lb::kSpinLimit; ++i)
+    if (mbar_try(b, parity)) return true;
+  return false;
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(shared_addr(bar))
+               : "memory");
+}
+// Matrix descriptor, 128-byte swizzle: lead = bytes between blocks of 64
+// N-values (N-major only), step = bytes between groups of eight 128-byte rows.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead, uint32_t step) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(step >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp32 accumulators, A and B fp16 or bf16; b_n_major: B is stored K by N
+template <class T>
+__device__ __forceinline__ constexpr uint32_t mma_shape(int M, int N, bool b_n_major) {
+  const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return 1u << 4 | f << 7 | f << 10 | (b_n_major ? 1u : 0u) << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(shape), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(shape), "r"(add)
+      : "memory");
+}
+// 32 columns of this thread's lane of tensor memory
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+// The registers of a load are good after this: passing them through keeps every use behind the wait.
+__device__ __forceinline__ void tmem_load_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int x, int row, int head, int page,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(shared_addr(dst)),
+      "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(shared_addr(bar))
+      : "memory");
+}
+
+// A block's part of one segment: key tiles t0 .. t1 - 1.
+template <int ROWS>
+struct Piece {
+  Walk<ROWS, kTile> w;
+  long long left;
+  int t0, t1;
+
+  __device__ __forceinline__ void begin(const AttendArgs& a, const Begin& b) {
+    left = b.u1 - b.u0;
+    w.start(a, b);
+    cut(a);
+  }
+  // Key tiles that no row of the tile sees are left out (a later part of a prompt's own keys).
+  __device__ __forceinline__ void cut(const AttendArgs& a) {
+    t0 = w.t;
+    t1 = (int)min((long long)w.kt, t0 + left);
+    left -= t1 - t0;
+    if (w.seq >= 0) {
+      const int last = min(w.r * ROWS + ROWS, w.count * a.group) - 1;
+      const int sees = min(w.len, w.before + last / a.group + 1);
+      t1 = max(t0, min(t1, (max(sees, 0) + kTile - 1) / kTile));
+    }
+  }
+  __device__ __forceinline__ bool next(const AttendArgs& a, const Begin& b) {
+    if (left <= 0) return false;
+    w.t = w.kt - 1;
+    w.next(a, b);
+    cut(a);
+    return true;
+  }
+};
+
+template <class T, int D, bool WIDE>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    many_rows_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v) {
+  constexpr int ROWS = WIDE ? 2 * kTile : kTile;
+  constexpr int R = kRing<D>, TB = kTileBytes<D>, HALF = kTile * 128;   // HALF: bytes of 64 columns of a tile
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (shared_addr(smem_raw) & 1023)) & 1023);
+  unsigned char* const qs = smem;            // [2] query tiles
+  unsigned char* const ring = smem + 2 * TB;
+  __shared__ __align__(8) uint64_t full[R], empty[R], s_full[2], p_full[2], o_full[2], q_full[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ long long plan_sm[28];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const Begin b = plan_block<kManyThreads, ROWS, kTile>(a, plan_sm);
+  if (b.u0 >= b.u1) return;   // the whole block
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(shared_addr(&tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&q_full[i], 4);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_slot;
+  bool dead = false;   // a wait ran out: go on without waiting, report, end
+  unsigned bad = 0;
+  // K tile number 2 n and V tile 2 n + 1 of the n-th key tile; tile x is in slot x % R
+  uint32_t n = 0;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    Piece<ROWS> pc;
+    pc.begin(a, b);
+    if (warp == 8) {
+      // ---- loads: lane i brings the i-th page of a tile
+      const int box = min(1 << a.page_shift, kTile);   // rows of a copy
+      uint32_t issued = 0;
+      do {
+        for (int t = pc.t0; t < pc.t1; ++t, ++n) {
+          const int key = t * kTile + lane * box;
+          const int held = min(kTile, pc.w.len - t * kTile);
+          const int boxes = (held + box - 1) / box;
+          int page = 0;
+          if (lane < boxes) {
+            page = pc.w.row[key >> a.page_shift];
+            if ((unsigned)page >= (unsigned)a.n_pages) {   // outside: the copy's fill, zeros
+              page = a.n_pages;
+              bad |= kStatusIndex;
+            }
+          }
+  #pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t x = 2 * n + kv;
+            const int slot = x % R;
+            if (x >= R && !dead && !mbar_wait(&empty[slot], (x / R - 1) & 1)) dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+            if (dead) break;
+            if (lane == 0) mbar_expect(&full[slot], boxes * box * D * 2);
+            __syncwarp();
+            issued = x + 1;
+            if (lane < boxes) {
+  #pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tma_page(ring + slot * TB + h * HALF + lane * box * 128, kv ? &map_v : &map_k, 64 * h,
+                         key & ((1 << a.page_shift) - 1), pc.w.h, page, &full[slot]);
+            }
+          }
+          if (dead) break;
+        }
+      } while (!dead && pc.next(a, b));
+      if (dead && lane == 0)   // copies under way land before the block ends
+        for (uint32_t x = issued > R ? issued - R : 0; x < issued; ++x) mbar_wait(&full[x % R], (x / R) & 1);
+    } else if (warp == 9) {
+      // ---- products
+      if (lane == 0) {
+        constexpr uint32_t qk = mma_shape<T>(kTile, kTile, false), pv = mma_shape<T>(kTile, D, true);
+        uint32_t steps[2] = {0, 0}, pieces[2] = {0, 0};
+        do {
+          const int tiles = pc.t1 - pc.t0, nv = WIDE ? 2 * tiles : tiles;
+          auto score = [&](int v) {   // S of step v
+            const int g = v & 1;
+            const uint32_t x = 2 * (n + (WIDE ? v >> 1 : v));
+            if (v < 2) {
+              if (!dead && !mbar_wait(&q_full[g], pieces[g] & 1)) dead = true;
+              ++pieces[g];
+            }
+            if (!dead && !mbar_wait(&full[x % R], (x / R) & 1)) dead = true;
+            tc_after();
+            const uint32_t q = shared_addr(qs + g * TB), k = shared_addr(ring + x % R * TB);
+  #pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+              const uint32_t off = (s >> 2) * HALF + (s & 3) * 32;
+              mma_ss(tmem + 128 * g, tile_desc(q + off, 16, 1024), tile_desc(k + off, 16, 1024), qk, s > 0);
+            }
+            tc_commit(&s_full[g]);
+            if (!WIDE || g == 1) tc_commit(&empty[x % R]);
+          };
+          if (nv > 0) score(0);
+          if (nv > 1) score(1);
+          for (int v = 0; v < nv; ++v) {
+            const int g = v & 1;
+            const uint32_t x = 2 * (n + (WIDE ? v >> 1 : v)) + 1;
+            if (!dead && !mbar_wait(&p_full[g], steps[g] & 1)) dead = true;
+            ++steps[g];
+            if (!dead && !mbar_wait(&full[x % R], (x / R) & 1)) dead = true;
+            tc_after();
+            const uint32_t vt = shared_addr(ring + x % R * TB);
+  #pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+              mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * s, tile_desc(vt + s * 2048, HALF, 1024), pv,
+                     v >= 2 || s > 0);
+            if (!WIDE || g == 1) tc_commit(&empty[x % R]);
+            if (v + 2 < nv) score(v + 2);
+            else tc_commit(&o_full[g]);
+          }
+          n += tiles;
+        } while (!dead && pc.next(a, b));
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    Piece<ROWS> pc;
+    pc.begin(a, b);
+    // ---- softmax group g, this thread's row
+    const int g = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + 128 * g + lane0, to = tmem + 256 + 128 * g + lane0;
+    const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);   // above 0, so that -inf stays -inf
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale turns the queries' signs
+    uint32_t steps = 0, pieces = 0;
+    do {
+      const int tiles = pc.t1 - pc.t0;
+      const int mine = WIDE ? tiles : (tiles - g + 1) / 2;   // steps of this group
+      const int at = pc.w.r * ROWS + (WIDE ? g * kTile : 0) + row;
+      const int tok = at / a.group;
+      const bool in = (pc.w.seq < 0 || tok < pc.w.count) && pc.w.first + tok < a.n_tokens;
+      const int lim = in ? (pc.w.seq < 0 ? pc.w.len : min(pc.w.len, pc.w.before + tok + 1)) : 0;
+      float m = -INFINITY, l = 0.f;
+      if (mine > 0) {
+        // the group's queries (their last readers, the products of the piece before, are done: o_full)
+        const unsigned char* src =
+            a.q + (long long)(pc.w.first + tok) * a.q_token + (long long)(pc.w.h * a.group + at - tok * a.group) * a.q_head;
+        unsigned char* dst = qs + g * TB + row * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 x = in ? *reinterpret_cast<const uint4*>(src + 16 * c) : make_uint4(0, 0, 0, 0);
+          x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * HALF + (((c & 7) ^ (row & 7)) << 4)) = x;
+        }
+        async_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[g]);
+        for (int j = 0; j < mine; ++j, ++steps) {
+          const int tile = WIDE ? j : 2 * j + g;
+          const int key = (pc.t0 + tile) * kTile;
+          if (!dead && !mbar_wait(&s_full[g], steps & 1)) dead = true;
+          dead = __any_sync(0xffffffffu, dead);
+          tc_after();
+          uint32_t s[kTile];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_load32(ts + 32 * c, s + 32 * c);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_load_wait(s + 32 * c);
+          if (__any_sync(0xffffffffu, key + kTile > lim)) {
+#pragma unroll
+            for (int i = 0; i < kTile; ++i)
+              if (key + i >= lim) s[i] = 0xff800000u;   // -inf
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+          top *= scale;
+          const bool raise = top > m + kRaise;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = raise ? exp2_fast(m - top) : 1.f;
+            if (raise) m = top;
+            l *= f;
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_load32(to + 32 * c, o);
+                tmem_load_wait(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_store32(to + 32 * c, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) {
+            const float p = exp2_fast(fmaf(__uint_as_float(s[i]), scale, -base));
+            sum += p;
+            s[i] = __float_as_uint(p);
+          }
+          l += sum;
+#pragma unroll
+          for (int i = 0; i < kTile / 2; ++i)
+            s[i] = Mma<T>::pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+          tmem_store32(ts, s);
+          tmem_store32(ts + 32, s + 32);
+          tmem_store_wait();
+          if (pc.w.len - key < kTile && (!WIDE || g == 0)) {   // V rows past the end
+            const uint32_t x = 2 * (n + tile) + 1;
+            if (!dead && !mbar_wait(&full[x % R], (x / R) & 1)) dead = true;
+            if (row >= pc.w.len - key) {
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(ring + x % R * TB + (c >> 3) * HALF + row * 128 + (c & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            async_fence();
+            dead = __any_sync(0xffffffffu, dead);
+          }
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[g]);
+        }
+        if (!dead && !mbar_wait(&o_full[g], pieces & 1)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        ++pieces;
+        tc_after();
+      }
+      // ---- the partial
+      const int rows_here = pc.w.seq < 0 ? (a.n_tokens - pc.w.first) * a.group : pc.w.count * a.group;
+      const long long slot = (pc.w.seg + (int)blockIdx.x) * (WIDE ? 1ll : 2ll) + (WIDE ? 0 : g);
+      const int r = (WIDE ? g * kTile : 0) + row;
+      const bool keep = at < rows_here && r < a.rows_alloc && slot < a.n_partials;
+      if (keep) a.ml[slot * a.rows_alloc + r] = make_float2(m, l);
+      if (mine > 0) {
+        float* dst = a.part + (slot * a.rows_alloc + r) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_load32(to + 32 * c, o);
+          tmem_load_wait(o);
+          if (keep)
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+        tc_before();
+      }
+      n += tiles;
+    } while (!dead && pc.next(a, b));
+  }
+  if (dead) bad |= lb::kStatusTimeout;
+  if (bad) atomicOr(a.status, bad);
+  __syncwarp();
+  tc_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
 // ------------------------------------------------------------------ the join
 
 // Where a key set's partials are: of one launch of a partial kernel.
@@ -567,6 +1011,7 @@ struct Source {
   const float2* ml;
   const float* part;
   int rows, rows_alloc, blocks, n_partials;   // query rows of a tile; blocks of the launch
+  int ways;                                   // partials of a slot
 };
 struct JoinArgs {
   Source prefix, own;   // head null: no such key set
@@ -600,10 +1045,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
     if (kt <= 0) return;
     const long long U = S.head->units, G = min((long long)S.blocks, U);
     const int c0 = (int)(((ua + 1) * G - 1) / U), c1 = (int)(((ua + kt) * G - 1) / U);
-    for (int c = c0; c <= c1; ++c) {
-      const long long at = (long long)(seg + c) * S.rows_alloc + row;
-      if (seg + c >= S.n_partials) continue;
+    for (int x = (seg + c0) * S.ways; x < (seg + c1 + 1) * S.ways; ++x) {
+      const long long at = (long long)x * S.rows_alloc + row;
+      if (x >= S.n_partials) continue;
       const float2 p = S.ml[at];
+      if (p.x == -INFINITY) continue;   // nothing seen; its output row need not have been written
       float v[E];
       if constexpr (E == 4) {
         const float4 x = *reinterpret_cast<const float4*>(S.part + at * D + lane * 4);
@@ -612,7 +1058,6 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
         const float2 x = *reinterpret_cast<const float2*>(S.part + at * D + lane * 2);
         v[0] = x.x, v[1] = x.y;
       }
-      if (p.x == -INFINITY) continue;   // nothing seen
       const float now = fmaxf(m, p.x);
       const float f0 = exp2_fast(m - now), f1 = exp2_fast(p.x - now);
       m = now;
@@ -659,16 +1104,17 @@ size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 // Work memory of one launch: [head][sequences][ml][partials].
 struct Region {
-  int blocks, rows, rows_alloc;
+  int blocks, rows, rows_alloc, ways;   // rows: query rows of a tile; 0: no such launch
   long long partials;
   size_t seqs, ml, part, bytes;
 };
-Region region(int rows, int blocks, int64_t segs, int64_t most_rows, int n, int D) {
+Region region(int rows, int ways, int blocks, int64_t segs, int64_t most_rows, int n, int D) {
   Region g;
   g.blocks = blocks;
   g.rows = rows;
   g.rows_alloc = (int)std::min<int64_t>(rows, most_rows);
-  g.partials = segs + blocks;
+  g.ways = ways;
+  g.partials = (segs + blocks) * ways;
   g.seqs = up(sizeof(PlanHead));
   g.ml = g.seqs + up(sizeof(SeqPlan) * (size_t)n);
   g.part = g.ml + up(sizeof(float2) * (size_t)g.partials * g.rows_alloc);
@@ -676,20 +1122,35 @@ Region region(int rows, int blocks, int64_t segs, int64_t most_rows, int n, int 
   return g;
 }
 
-// Segments of the two key sets at most, with tiles of `rows` query rows.
-int64_t prefix_segs(int64_t heads, int64_t group, int64_t tokens, int rows) {
-  return heads * ((tokens * group + rows - 1) / rows);
-}
-int64_t own_segs(int64_t heads, int64_t group, int64_t tokens, int64_t n, int64_t most_q, int rows) {
-  const int64_t one = (most_q * group + rows - 1) / rows;
-  return heads * std::min(n * one, n + (tokens * group + rows - 1) / rows);
-}
-
-Region few_region(int heads, int group, int n_tokens, int n, int most_q, bool with_prefix, int D) {
-  const int64_t segs = (with_prefix ? prefix_segs(heads, group, n_tokens, kFewRows) : 0) +
-                       own_segs(heads, group, n_tokens, n, most_q, kFewRows);
-  const int64_t most = (int64_t)group * std::max(with_prefix ? n_tokens : 0, most_q);
-  return region(kFewRows, 2 * sm_count(), segs, most, n, D);
+// Which launch takes what.  The rows that read a key set decide: up to 16 go
+// to the few-rows kernel (its one tile), more to the many-rows kernel.
+struct Split {
+  bool few_prefix, few_own, many_prefix, many_own, wide;
+  Region few, many;
+};
+Split split_of(int heads, int group, int n_tokens, int n, int most_q, bool with_prefix, int D) {
+  Split s{};
+  const int64_t p_rows = (int64_t)n_tokens * group, o_rows = (int64_t)most_q * group;
+  s.few_prefix = with_prefix && p_rows <= kFewRows;
+  s.many_prefix = with_prefix && !s.few_prefix;
+  s.few_own = o_rows <= kFewRows;
+  s.many_own = !s.few_own;
+  // segments of the two key sets at most, with tiles of `rows` query rows
+  auto segs = [&](int rows, bool prefix, bool own) -> int64_t {
+    const int64_t one = (o_rows + rows - 1) / rows;
+    return (int64_t)heads * ((prefix ? (p_rows + rows - 1) / rows : 0) +
+                             (own ? std::min<int64_t>(n * one, n + (p_rows + rows - 1) / rows) : 0));
+  };
+  if (s.few_prefix || s.few_own)
+    s.few = region(kFewRows, 1, 2 * sm_count(), segs(kFewRows, s.few_prefix, s.few_own),
+                   std::max(s.few_prefix ? p_rows : 0, s.few_own ? o_rows : 0), n, D);
+  if (s.many_prefix || s.many_own) {
+    const int64_t most = std::max(s.many_prefix ? p_rows : 0, s.many_own ? o_rows : 0);
+    s.wide = most > kTile;
+    const int rows = s.wide ? 2 * kTile : kTile;
+    s.many = region(rows, s.wide ? 1 : 2, sm_count(), segs(rows, s.many_prefix, s.many_own), most, n, D);
+  }
+  return s;
 }
 
 template <class K>
@@ -701,13 +1162,63 @@ cudaError_t allow_smem(K kern, lb::PerDevice& slot, int bytes) {
   }));
 }
 
-template <class T, int D>
-cudaError_t launch(const AttendArgs& few, int blocks, const JoinArgs& join, cudaStream_t st) {
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// A plane as (width, rows of a page, heads, pages); a copy brings 64 columns
+// of a page's rows, 128 at most, into 128-byte rows with the 128-byte swizzle.
+lb_status plane_map(const lb_cache& c, const lb_plane& P, CUtensorMap* map) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return lb::cuda_fail(cudaErrorNotSupported);
+  const int64_t row = 2 * P.width;
+  auto stride = [&](int64_t s, int64_t extent) -> cuuint64_t { return (cuuint64_t)(extent > 1 ? 2 * s : row); };
+  const cuuint64_t dim[4] = {(cuuint64_t)P.width, (cuuint64_t)c.page_size, (cuuint64_t)P.heads, (cuuint64_t)c.n_pages};
+  const cuuint64_t st[3] = {stride(P.stride_row, c.page_size), stride(P.stride_head, P.heads),
+                            stride(P.stride_page, c.n_pages)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(c.page_size, kTile), 1, 1}, one[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, P.dt == LB_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                        P.data, dim, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LB_OK : LB_ERR_SHAPE;   // strides that the copy engine does not take
+}
+
+template <class T, int D, bool WIDE>
+cudaError_t launch_many(const AttendArgs& a, int blocks, const CUtensorMap& k, const CUtensorMap& v,
+                        cudaStream_t st) {
   static lb::PerDevice smem;
-  cudaError_t e = allow_smem(few_rows_kernel<T, D>, smem, kFewSmem<D>);
+  const cudaError_t e = allow_smem(many_rows_kernel<T, D, WIDE>, smem, kManySmem<D>);
   if (e != cudaSuccess) return e;
-  few_rows_kernel<T, D><<<blocks, kFewThreads, kFewSmem<D>, st>>>(few);
-  e = cudaGetLastError();
+  many_rows_kernel<T, D, WIDE><<<blocks, kManyThreads, kManySmem<D>, st>>>(a, k, v);
+  return cudaGetLastError();
+}
+
+template <class T, int D>
+cudaError_t launch(const Split& s, const AttendArgs& few, const AttendArgs& many, const CUtensorMap& k,
+                   const CUtensorMap& v, const JoinArgs& join, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (s.many.rows)
+    e = s.wide ? launch_many<T, D, true>(many, s.many.blocks, k, v, st)
+               : launch_many<T, D, false>(many, s.many.blocks, k, v, st);
+  if (e == cudaSuccess && s.few.rows) {
+    static lb::PerDevice smem;
+    e = allow_smem(few_rows_kernel<T, D>, smem, kFewSmem<D>);
+    if (e != cudaSuccess) return e;
+    few_rows_kernel<T, D><<<s.few.blocks, kFewThreads, kFewSmem<D>, st>>>(few);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   join_kernel<T, D><<<dim3(join.n_tokens, lb::ceil_div(join.heads * join.group, 8)), 256, 0, st>>>(join);
   return cudaGetLastError();
@@ -733,8 +1244,9 @@ size_t littlebit_cache_attend_work(const lb_cache* c, int k, int heads_q, int n_
                                    int with_prefix) {
   if (check_attend(c, k, heads_q, n_tokens, n, most_q) != LB_OK) return 0;
   const lb_plane& K = c->planes[k];
-  return few_region(K.heads, heads_q / K.heads, n_tokens, n, std::min(most_q, std::max(n_tokens, 1)),
-                    with_prefix != 0, K.width).bytes;
+  const Split s = split_of(K.heads, heads_q / K.heads, n_tokens, n, std::min(most_q, std::max(n_tokens, 1)),
+                           with_prefix != 0, K.width);
+  return s.few.bytes + s.many.bytes;
 }
 
 lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows* q, int n_tokens,
@@ -755,13 +1267,15 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   if (reinterpret_cast<uintptr_t>(work) % 256) return LB_ERR_ALIGN;
   const int D = K.width, group = q->heads / K.heads;
   most_q = std::min(most_q, n_tokens);
-  const Region g = few_region(K.heads, group, n_tokens, n, most_q, prefix >= 0, D);
-  if (work_bytes < g.bytes) return LB_ERR_SHAPE;
+  const Split s = split_of(K.heads, group, n_tokens, n, most_q, prefix >= 0, D);
+  if (work_bytes < s.few.bytes + s.many.bytes) return LB_ERR_SHAPE;
+  if (s.few.partials > INT32_MAX || s.many.partials > INT32_MAX) return LB_ERR_SHAPE;
+  CUtensorMap map_k{}, map_v{};
+  if (s.many.rows && ((r = plane_map(*c, K, &map_k)) != LB_OK || (r = plane_map(*c, V, &map_v)) != LB_OK)) return r;
   unsigned* status = nullptr;
   cudaError_t e = lb::touch_cache_status(&status);
   if (e != cudaSuccess) return lb::cuda_fail(e);
 
-  unsigned char* w = static_cast<unsigned char*>(work);
   AttendArgs a{};
   a.k = PlaneArg{static_cast<const unsigned char*>(K.data), 2 * K.stride_page, 2 * K.stride_head, 2 * K.stride_row};
   a.v = PlaneArg{static_cast<const unsigned char*>(V.data), 2 * V.stride_page, 2 * V.stride_head, 2 * V.stride_row};
@@ -784,19 +1298,26 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   a.heads = K.heads;
   a.group = group;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.do_prefix = prefix >= 0;
-  a.do_own = 1;
-  a.head = reinterpret_cast<PlanHead*>(w);
-  a.seqs = reinterpret_cast<SeqPlan*>(w + g.seqs);
-  a.ml = reinterpret_cast<float2*>(w + g.ml);
-  a.part = reinterpret_cast<float*>(w + g.part);
-  a.rows_alloc = g.rows_alloc;
-  a.n_partials = (int)g.partials;
   a.status = status;
   JoinArgs j{};
-  const Source s{a.head, a.seqs, a.ml, a.part, g.rows, g.rows_alloc, g.blocks, (int)g.partials};
-  j.own = s;
-  if (prefix >= 0) j.prefix = s;
+  auto place = [&](const Region& g, unsigned char* w, bool own, bool with_prefix) {
+    AttendArgs x = a;
+    x.do_prefix = with_prefix;
+    x.do_own = own;
+    x.head = reinterpret_cast<PlanHead*>(w);
+    x.seqs = reinterpret_cast<SeqPlan*>(w + g.seqs);
+    x.ml = reinterpret_cast<float2*>(w + g.ml);
+    x.part = reinterpret_cast<float*>(w + g.part);
+    x.rows_alloc = g.rows_alloc;
+    x.n_partials = (int)g.partials;
+    const Source src{x.head, x.seqs, x.ml, x.part, g.rows, g.rows_alloc, g.blocks, (int)g.partials, g.ways};
+    if (own) j.own = src;
+    if (with_prefix) j.prefix = src;
+    return x;
+  };
+  unsigned char* w = static_cast<unsigned char*>(work);
+  const AttendArgs few = place(s.few, w, s.few_own, s.few_prefix);
+  const AttendArgs many = place(s.many, w + s.few.bytes, s.many_own, s.many_prefix);
   j.out = static_cast<unsigned char*>(out->data);
   j.out_token = 2 * out->stride_token;
   j.out_head = 2 * out->stride_head;
@@ -806,9 +1327,11 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   j.group = group;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (K.dt == LB_F16)
-    e = D == 128 ? launch<__half, 128>(a, g.blocks, j, st) : launch<__half, 64>(a, g.blocks, j, st);
+    e = D == 128 ? launch<__half, 128>(s, few, many, map_k, map_v, j, st)
+                 : launch<__half, 64>(s, few, many, map_k, map_v, j, st);
   else
-    e = D == 128 ? launch<__nv_bfloat16, 128>(a, g.blocks, j, st) : launch<__nv_bfloat16, 64>(a, g.blocks, j, st);
+    e = D == 128 ? launch<__nv_bfloat16, 128>(s, few, many, map_k, map_v, j, st)
+                 : launch<__nv_bfloat16, 64>(s, few, many, map_k, map_v, j, st);
   return e == cudaSuccess ? LB_OK : lb::cuda_fail(e);
 }
 
