@@ -8,17 +8,17 @@
 // handled once for the rows of all sequences, a sequence's own tokens another,
 // and both are cut further to share the work out evenly.
 //
-// Work.  A segment is (K and V head, tile of query rows, key set); a unit is
-// one key tile of one segment.  The query rows of a tile are (token, query
-// head of the group) pairs, so that a K and V head is read once for its whole
-// group.  The units of all segments lie in a row, and block c of G (the
-// grid, or U if that is less) takes units [U c / G, U (c + 1) / G): every block gets the same amount to within one
-// unit, whatever the lengths.  A block writes one fp32 partial for each segment
-// that it touches, at slot segment + c (unique, since along the row of units
-// one of the two grows from partial to partial), and join_kernel adds a row's
-// partials in the order of their blocks: the result does not depend on timing.
-// The lengths are read on the device, so a captured graph follows a growing
-// cache.
+// Work.  A segment is (K and V head, tile of query rows, key set), its query
+// rows being (token, query head of the group) pairs, so that a K and V head is
+// read once for its whole group.  A segment's extent counts what it costs: its
+// key tiles, and a few units for its beginning and end.  The extents of all
+// segments lie in a row of U units, and with W = ceil(U / grid) block c takes
+// units [c W, (c + 1) W): every block gets the same amount of work whatever the
+// lengths.  A block writes one fp32 partial for each segment that it touches,
+// at slot segment + c (unique, since along the row of units one of the two grows
+// from partial to partial), and join_kernel adds a row's partials in the order
+// of their blocks: the result does not depend on timing.  The lengths are read
+// on the device, so a captured graph follows a growing cache.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -26,13 +26,24 @@
 
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "lb_internal.h"
 
 namespace {
 
 constexpr unsigned kStatusIndex = 1u << LB_ERR_INDEX;
+
+// How a kernel cuts its segments: query rows of a tile, keys of a tile, units
+// that a segment's beginning and end are worth, units of one key tile.
+struct FewCut {
+  static constexpr int kRows = 16, kKeys = 64, kSetup = 1;
+  static __device__ __forceinline__ int cost(int) { return 1; }
+};
+struct ManyCut {
+  static constexpr int kRows = 256, kKeys = 128, kSetup = 3;
+  // up to 128 rows take half of the products (see many_rows_kernel)
+  static __device__ __forceinline__ int cost(int rows) { return rows > 128 ? 2 : 1; }
+};
 
 // A plane of one cache, strides in bytes.
 struct PlaneArg {
@@ -42,17 +53,17 @@ struct PlaneArg {
 
 // What both the partial kernels and the join know of a launch.
 struct PlanHead {
-  long long units;       // all units of the launch
-  int t0, t1;            // tokens of the batch
-  int p_segs, p_kt, p_rt;   // prefix: segments, key tiles and row tiles a segment
-  int pad;
+  long long width;          // units of a block
+  int t0, t1;               // tokens of the batch
+  int p_rows, p_rt, p_kt;   // prefix: query rows, row tiles a head, key tiles
+  int p_head;               // units of one head's segments
 };
 struct SeqPlan {
   long long units_before;   // units of the launch before this sequence's (the prefix's included)
   int segs_before;          // segments before this sequence's (the prefix's included)
   int first, count;         // tokens
-  int kt, rt;               // key tiles and row tiles a segment
-  int pad;
+  int len, before;          // see Seq
+  int head;                 // units of one head's segments
 };
 
 struct AttendArgs {
@@ -71,8 +82,8 @@ struct AttendArgs {
   int do_prefix, do_own;       // which key sets this launch takes
   PlanHead* head;              // written by block 0 for the join
   SeqPlan* seqs;
-  float2* ml;                  // [slot][rows_alloc] maximum (times log2 e) and sum
-  float* part;                 // [slot][rows_alloc][D]
+  float2* ml;                  // [partial][rows_alloc] maximum (times log2 e) and sum
+  float* part;                 // [partial][rows_alloc][D]
   int rows_alloc, n_partials;
   unsigned* status;
 };
@@ -109,17 +120,37 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int i) {
   return s;
 }
 
-template <int ROWS, int KEYS>
-__device__ __forceinline__ void seq_tiles(const AttendArgs& a, const Seq& s, int& rt, int& kt) {
-  rt = (s.count * a.group + ROWS - 1) / ROWS;
-  kt = (int)(((long long)s.len + KEYS - 1) / KEYS);
+template <class C>
+__device__ __forceinline__ int row_tiles(int rows) {
+  return (rows + C::kRows - 1) / C::kRows;
+}
+// Key tiles that row tile r of a sequence sees any key of, and its segment's extent.
+template <class C>
+__device__ __forceinline__ int own_tiles(int count, int group, int len, int before, int r) {
+  const int last = (min((r + 1) * C::kRows, count * group) - 1) / group;
+  const int sees = min(len, max(before + last + 1, 0));
+  return (int)(((long long)sees + C::kKeys - 1) / C::kKeys);
+}
+template <class C>
+__device__ __forceinline__ int extent(int tiles, int rows_left) {
+  return tiles ? C::kSetup + tiles * C::cost(rows_left) : 0;
+}
+template <class C>
+__device__ __forceinline__ int own_extent(int count, int group, int len, int before, int r) {
+  return extent<C>(own_tiles<C>(count, group, len, before, r), count * group - r * C::kRows);
+}
+// Units of one head's segments of a sequence.
+template <class C>
+__device__ __forceinline__ int own_head(int count, int group, int len, int before) {
+  int sum = 0;
+  for (int r = 0, n = row_tiles<C>(count * group); r < n; ++r) sum += own_extent<C>(count, group, len, before, r);
+  return sum;
 }
 
-// Where a block begins: the totals, and the sequence (or the prefix: -1) its first unit lies in.
+// Where a block begins.
 struct Begin {
-  long long units, u0, u1;   // all units; this block's
-  int p_segs, p_kt, p_rt, t0;
-  int p_len;
+  long long u0, u1;          // its units
+  int p_rt, p_kt, p_rows, p_head, p_len, t0;
   int seq;                   // sequence of u0; -1: the prefix
   long long seq_u;           // units before it
   int seq_segs;              // segments before it
@@ -128,53 +159,56 @@ struct Begin {
 // Run by the whole block (THREADS threads).  Two sweeps over the sequences,
 // THREADS at a time: the total, then the place of u0.  Block 0 leaves the
 // plan for join_kernel.
-template <int THREADS, int ROWS, int KEYS>
-__device__ __forceinline__ Begin plan_block(const AttendArgs& a, long long* sm /* THREADS/32 * 2 + 4 */) {
+template <class C, int THREADS>
+__device__ __forceinline__ Begin plan_block(const AttendArgs& a, long long* sm /* THREADS / 32 * 2 + 3 */) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Begin b;
   b.t0 = min(max(a.starts[0], 0), a.n_tokens);
   const int t1 = min(max(a.starts[a.n], b.t0), a.n_tokens);
-  b.p_segs = b.p_kt = b.p_rt = b.p_len = 0;
+  b.p_rows = b.p_rt = b.p_kt = b.p_len = b.p_head = 0;
   if (a.do_prefix) {
     const long long cap = (long long)a.max_pages << a.page_shift;
     b.p_len = (int)min((long long)max(a.length[a.prefix], 0), cap);
-    b.p_rt = (int)(((long long)(t1 - b.t0) * a.group + ROWS - 1) / ROWS);
-    b.p_kt = (int)(((long long)b.p_len + KEYS - 1) / KEYS);
-    b.p_segs = b.p_rt * a.heads;
+    b.p_rows = (t1 - b.t0) * a.group;
+    b.p_rt = row_tiles<C>(b.p_rows);
+    b.p_kt = (int)(((long long)b.p_len + C::kKeys - 1) / C::kKeys);
+    if (b.p_rt)
+      b.p_head = (b.p_rt - 1) * extent<C>(b.p_kt, C::kRows) + extent<C>(b.p_kt, b.p_rows - (b.p_rt - 1) * C::kRows);
   }
-  const long long p_units = (long long)b.p_segs * b.p_kt;
+  const long long p_units = (long long)b.p_head * a.heads;
+  const long long p_segs = (long long)b.p_rt * a.heads;
   long long* warp_u = sm;
   long long* warp_s = sm + W;
   long long* found = sm + 2 * W;   // sequence, units before, segments before
   long long total = p_units;
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1) {
-      b.units = total;
-      // with fewer units than blocks the last blocks have none: a block inside a segment always has a unit
-      const long long blocks = min((long long)gridDim.x, total);
-      b.u0 = blockIdx.x < blocks ? total * blockIdx.x / blocks : total;
-      b.u1 = blockIdx.x < blocks ? total * (blockIdx.x + 1) / blocks : total;
+      // every block but the last ones has the same number of units; a block inside a segment always has some
+      const long long width = max((total + gridDim.x - 1) / gridDim.x, 1ll);
+      b.u0 = min(width * blockIdx.x, total);
+      b.u1 = min(width * (blockIdx.x + 1), total);
       b.seq = -1;
       b.seq_u = 0;
       b.seq_segs = 0;
-      if (blockIdx.x == 0 && tid == 0) *a.head = PlanHead{total, b.t0, t1, b.p_segs, b.p_kt, b.p_rt, 0};
+      if (blockIdx.x == 0 && tid == 0) *a.head = PlanHead{width, b.t0, t1, b.p_rows, b.p_rt, b.p_kt, b.p_head};
       if (b.u0 < p_units || b.u0 >= b.u1) break;
     }
     long long u = p_units;
-    long long segs = b.p_segs;
+    long long segs = p_segs;
     if (a.do_own)
       for (int i0 = 0; i0 < a.n; i0 += THREADS) {
         const int i = i0 + tid;
-        int rt = 0, kt = 0;
+        int head = 0, rt = 0;
         Seq s{};
         if (i < a.n) {
           s = load_seq(a, i);
-          seq_tiles<ROWS, KEYS>(a, s, rt, kt);
+          rt = row_tiles<C>(s.count * a.group);
+          head = own_head<C>(s.count, a.group, s.len, s.before);
           if (s.slot != -1 && (s.slot < 0 || s.slot >= a.n_slots) && blockIdx.x == 0)
             atomicOr(a.status, kStatusIndex);
         }
-        const long long mine = (long long)rt * kt * a.heads, mine_s = (long long)rt * a.heads;
+        const long long mine = (long long)head * a.heads, mine_s = (long long)rt * a.heads;
         long long xu = mine, xs = mine_s;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -200,7 +234,8 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a, long long* sm /
           segs += warp_s[w];
         }
         if (pass == 0) {
-          if (blockIdx.x == 0 && i < a.n) a.seqs[i] = SeqPlan{before_u, (int)before_s, s.first, s.count, kt, rt, 0};
+          if (blockIdx.x == 0 && i < a.n)
+            a.seqs[i] = SeqPlan{before_u, (int)before_s, s.first, s.count, s.len, s.before, head};
         } else if (i < a.n && b.u0 >= before_u && b.u0 < before_u + mine) {
           found[0] = i;
           found[1] = before_u;
@@ -218,61 +253,99 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a, long long* sm /
   return b;
 }
 
-// Walks a block's units in order.  Every warp keeps its own (the values are
-// the same in all of them).
-template <int ROWS, int KEYS>
-struct Walk {
-  int seq;        // -1: the prefix
-  int h, r, t;    // head, row tile, key tile
-  int rt, kt;
-  int seg;        // segment number
-  int first, count, len, before;
-  const int* row; // page table row
+// A block's part of one segment, key tiles t0 .. t1 - 1 (there may be none),
+// and the walk to the next.  Every warp keeps its own; the values are the same
+// in all of them.
+template <class C>
+struct Piece {
+  int seq;                   // -1: the prefix
+  int h, r, rt;              // head, row tile, row tiles a head
+  int seg;                   // segment number
+  int rows;                  // query rows of the key set
+  int first, len, before;    // first token; keys; keys before the first token
+  int kt;                    // key tiles of the segment
+  const int* table;          // page table row
+  int t0, t1;
+  long long left;            // units of the block still to come
+
+  __device__ __forceinline__ int rows_left() const { return rows - r * C::kRows; }
+  // Keys that token `tok` of the key set sees.
+  __device__ __forceinline__ int sees(int tok) const { return seq < 0 ? len : min(len, before + tok + 1); }
 
   __device__ __forceinline__ void enter(const AttendArgs& a, const Begin& b) {
     if (seq < 0) {
       rt = b.p_rt;
-      kt = b.p_kt;
+      rows = b.p_rows;
       first = b.t0;
-      count = 0;
       len = before = b.p_len;
-      row = a.table + a.prefix * a.table_stride;
+      table = a.table + a.prefix * a.table_stride;
     } else {
       const Seq s = load_seq(a, seq);
-      seq_tiles<ROWS, KEYS>(a, s, rt, kt);
+      rows = s.count * a.group;
+      rt = row_tiles<C>(rows);
       first = s.first;
-      count = s.count;
       len = s.len;
       before = s.before;
-      row = a.table + s.slot * a.table_stride;
+      table = a.table + s.slot * a.table_stride;
     }
   }
-  __device__ __forceinline__ void start(const AttendArgs& a, const Begin& b) {
+  __device__ __forceinline__ int tile(const AttendArgs& a, const Begin& b) {   // the extent
+    kt = seq < 0 ? b.p_kt : own_tiles<C>(rows / a.group, a.group, len, before, r);
+    return extent<C>(kt, rows_left());
+  }
+  // Units x .. ext - 1 of the segment, as far as they are this block's.
+  __device__ __forceinline__ void cut(int x, int ext) {
+    const int n = (int)min((long long)(ext - x), left);
+    left -= n;
+    const int c = C::cost(rows_left());
+    t0 = max(x - C::kSetup + c - 1, 0) / c;
+    t1 = max(x + n - C::kSetup + c - 1, 0) / c;
+  }
+  __device__ __forceinline__ void begin(const AttendArgs& a, const Begin& b) {
+    left = b.u1 - b.u0;
     seq = b.seq;
     enter(a, b);
     const long long off = b.u0 - b.seq_u;
-    const int s = (int)(off / kt);
-    t = (int)(off - (long long)s * kt);
-    h = s / rt;
-    r = s - h * rt;
-    seg = b.seq_segs + s;
-  }
-  __device__ __forceinline__ void next(const AttendArgs& a, const Begin& b) {
-    if (++t < kt) return;
-    t = 0;
-    ++seg;
-    if (++r < rt) return;
+    const int head = seq < 0 ? b.p_head : own_head<C>(rows / a.group, a.group, len, before);
+    h = (int)(off / max(head, 1));
+    int x = (int)(off - (long long)h * head);
     r = 0;
-    if (++h < a.heads) return;
-    h = 0;
+    if (seq < 0) {
+      const int e = extent<C>(b.p_kt, C::kRows);
+      r = min(x / e, rt - 1);
+      x -= r * e;
+    }
+    int ext = tile(a, b);
+    while (x >= ext && r + 1 < rt) {
+      x -= ext;
+      ++r;
+      ext = tile(a, b);
+    }
+    seg = b.seq_segs + h * rt + r;
+    cut(x, ext);
+  }
+  __device__ __forceinline__ bool next(const AttendArgs& a, const Begin& b) {
+    if (left <= 0) return false;
+    int ext;
     do {
-      if (++seq >= a.n) {
-        seq = a.n;
-        return;
+      ++seg;
+      if (++r == rt) {
+        r = 0;
+        if (++h == a.heads) {
+          h = 0;
+          do {
+            if (++seq >= a.n) {   // lengths that changed under way
+              left = 0;
+              return false;
+            }
+            enter(a, b);
+          } while (rt == 0);
+        }
       }
-      enter(a, b);
-      if (kt == 0) seg += rt * a.heads;   // no keys: its segments have no units
-    } while (kt == 0 || rt == 0);
+      ext = tile(a, b);
+    } while (ext == 0);
+    cut(0, ext);
+    return true;
   }
 };
 
@@ -289,7 +362,7 @@ struct Walk {
 // mma.sync is enough here: a tile's two products take about 600 cycles of the
 // 1400 in which HBM delivers it to an SM.  The four partials are joined through
 // shared memory when a segment ends.
-constexpr int kFewRows = 16, kFewKeys = 64, kFewThreads = 128;
+constexpr int kFewRows = FewCut::kRows, kFewKeys = FewCut::kKeys, kFewThreads = 128;
 
 template <int D> constexpr int kFewStages = D == 128 ? 3 : 6;
 template <int D> constexpr int kFewStage = 2 * 16 * D * 2;   // bytes of a warp's stage: K and V rows of 16 keys
@@ -348,37 +421,42 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   __shared__ float2 stat[4][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const Begin b = plan_block<kFewThreads, kFewRows, kFewKeys>(a, plan_sm);
+  const Begin b = plan_block<FewCut, kFewThreads>(a, plan_sm);
   if (b.u0 >= b.u1) return;
   const uint32_t ring = shared_addr(smem) + warp * S * kFewStage<D>;
   float* joined = reinterpret_cast<float*>(smem + 4 * S * kFewStage<D>);
-  using W = Walk<kFewRows, kFewKeys>;
 
-  // ---- loads: page numbers one unit ahead of the copies, copies S - 1 units ahead of the products
-  W lw;
-  lw.start(a, b);
-  long long l_left = b.u1 - b.u0;
+  // ---- loads: page numbers one tile ahead of the copies, copies S - 1 tiles ahead of the products
+  Piece<FewCut> lp;
+  lp.begin(a, b);
+  int lt = lp.t0;   // next tile to copy
+  bool more = true;
   int page[2] = {0, 0};
   auto fetch_pages = [&]() {
-    const int key = lw.t * kFewKeys + 16 * warp;
+    while (more && lt >= lp.t1) {
+      more = lp.next(a, b);
+      lt = lp.t0;
+    }
+    if (!more) return;
+    const int key = lt * kFewKeys + 16 * warp;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) page[i] = key + 8 * i < lw.len ? lw.row[(key + 8 * i) >> a.page_shift] : 0;
+    for (int i = 0; i < 2; ++i) page[i] = key + 8 * i < lp.len ? lp.table[(key + 8 * i) >> a.page_shift] : 0;
   };
   fetch_pages();
   unsigned bad = 0;
   auto issue = [&](int stage) {
-    if (l_left > 0) {
-      const int key = lw.t * kFewKeys + 16 * warp;
-      if (key < lw.len) {
+    if (more) {
+      const int key = lt * kFewKeys + 16 * warp;
+      if (key < lp.len) {
         const uint32_t dst = ring + stage * kFewStage<D>;
-        const long long head_k = lw.h * a.k.stride_head, head_v = lw.h * a.v.stride_head;
+        const long long head_k = lp.h * a.k.stride_head, head_v = lp.h * a.v.stride_head;
 #pragma unroll
         for (int i = 0; i < CH / 2; ++i) {
           const int row = (i * 32 + lane) / CH, ch = lane % CH;
           const int p = page[row >> 3];
           const bool in = (unsigned)p < (unsigned)a.n_pages;
           if (!in) bad = kStatusIndex;
-          const bool use = in && key + row < lw.len;
+          const bool use = in && key + row < lp.len;
           const long long off = use ? (key + row) & ((1 << a.page_shift) - 1) : 0;
           const long long pg = use ? p : 0;
           const uint32_t at = dst + row * (2 * D) + ((ch ^ (row & 7)) << 4);
@@ -386,177 +464,168 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
           copy16(at + 32 * D, a.v.data + pg * a.v.stride_page + off * a.v.stride_row + head_v + 16 * ch, use ? 16 : 0);
         }
       }
-      if (--l_left > 0) {
-        lw.next(a, b);
-        fetch_pages();
-      }
+      ++lt;
+      fetch_pages();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) issue(s);
 
-  W w;
-  w.start(a, b);
-  long long left = b.u1 - b.u0;
+  Piece<FewCut> w;
+  w.begin(a, b);
   uint32_t qf[D / 16][4];
   float o[D / 8][4];
   float m[2], l[2];
   int lim[2];   // keys that rows g and g + 8 see
   int stage = 0;
-  bool fresh = true;
-  while (left > 0) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-    __syncwarp();
-    issue(stage == 0 ? S - 1 : stage - 1);
-    if (fresh) {   // a new segment: its query rows
-      fresh = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = w.r * kFewRows + g + 8 * i;
-        const int tok = row / a.group;
-        const int n_tok = w.seq < 0 ? 0x7fffffff : w.count;
-        const bool in = tok < n_tok && w.first + tok < a.n_tokens;
-        lim[i] = in ? (w.seq < 0 ? w.len : min(w.len, w.before + tok + 1)) : 0;
-        const unsigned char* src =
-            a.q + (long long)(w.first + tok) * a.q_token + (long long)(w.h * a.group + row - tok * a.group) * a.q_head;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          qf[k][i] = in ? *reinterpret_cast<const uint32_t*>(src + k * 32 + c * 4) : 0;
-          qf[k][i + 2] = in ? *reinterpret_cast<const uint32_t*>(src + k * 32 + 16 + c * 4) : 0;
-        }
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  do {
+    const int slot = w.seg + (int)blockIdx.x;
+    const int rows = slot < a.n_partials ? min(min(kFewRows, a.rows_alloc), w.rows_left()) : 0;
+    if (w.t0 == w.t1) {   // units of the segment's beginning only
+      if (threadIdx.x < rows) a.ml[(long long)slot * a.rows_alloc + threadIdx.x] = make_float2(-INFINITY, 0.f);
+      continue;
     }
-    const int key = w.t * kFewKeys + 16 * warp;
-    if (key < w.len) {
-      const uint32_t kb = ring + stage * kFewStage<D>, vb = kb + 32 * D;
-      float s[2][4] = {};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = w.r * kFewRows + g + 8 * i;
+      const int tok = row / a.group;
+      const bool in = row < w.rows;
+      lim[i] = in ? w.sees(tok) : 0;
+      const unsigned char* src =
+          a.q + (long long)(w.first + tok) * a.q_token + (long long)(w.h * a.group + row - tok * a.group) * a.q_head;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        uint32_t f[4];
-        const int row = ((lane >> 4) << 3) + (lane & 7), ch = 2 * k + ((lane >> 3) & 1);
-        ldmatrix4<false>(f, kb + row * (2 * D) + ((ch ^ (row & 7)) << 4));
-        Mma<T>::run(s[0], qf[k], f[0], f[1]);
-        Mma<T>::run(s[1], qf[k], f[2], f[3]);
+        qf[k][i] = in ? *reinterpret_cast<const uint32_t*>(src + k * 32 + c * 4) : 0;
+        qf[k][i + 2] = in ? *reinterpret_cast<const uint32_t*>(src + k * 32 + 16 + c * 4) : 0;
       }
-      // scores in units of log 2; keys a row does not see get -inf
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = key + 8 * n + 2 * c + (e & 1);
-          s[n][e] = at < lim[e >> 1] ? s[n][e] * a.scale_log2 : -INFINITY;
-          top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
-        }
-      float alpha[2], base[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-        const float now = fmaxf(m[i], top[i]);
-        base[i] = now == -INFINITY ? 0.f : now;
-        alpha[i] = exp2_fast(m[i] - base[i]);
-        m[i] = now;
-      }
-      float sum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][e] = exp2_fast(s[n][e] - base[e >> 1]);
-          sum[e >> 1] += s[n][e];
-        }
-      l[0] = l[0] * alpha[0] + sum[0];
-      l[1] = l[1] * alpha[1] + sum[1];
-      const uint32_t p[4] = {Mma<T>::pack(s[0][0], s[0][1]), Mma<T>::pack(s[0][2], s[0][3]),
-                             Mma<T>::pack(s[1][0], s[1][1]), Mma<T>::pack(s[1][2], s[1][3])};
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1];
-          o[i][3] *= alpha[1];
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        uint32_t f[4];
-        const int row = lane & 15, ch = 2 * d + (lane >> 4);
-        ldmatrix4<true>(f, vb + row * (2 * D) + ((ch ^ (row & 7)) << 4));
-        Mma<T>::run(o[2 * d], p, f[0], f[1]);
-        Mma<T>::run(o[2 * d + 1], p, f[2], f[3]);
-      }
+      m[i] = -INFINITY;
+      l[i] = 0.f;
     }
-    stage = stage + 1 == S ? 0 : stage + 1;
-    --left;
-    const bool last = w.t + 1 == w.kt || left == 0;
-    if (last) {
-      // ---- join the four warps' partials and write the segment's
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if (c == 0) stat[warp][g + 8 * i] = make_float2(m[i], l[i]);
-      }
-      __syncthreads();
-      float f[2];
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int t = w.t0; t < w.t1; ++t) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+      __syncwarp();
+      issue(stage == 0 ? S - 1 : stage - 1);
+      const int key = t * kFewKeys + 16 * warp;
+      if (key < w.len) {
+        const uint32_t kb = ring + stage * kFewStage<D>, vb = kb + 32 * D;
+        float s[2][4] = {};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) top = fmaxf(top, stat[x][g + 8 * i].x);
-        f[i] = top == -INFINITY ? 0.f : exp2_fast(m[i] - top);
-      }
-      const int slot = w.seg + (int)blockIdx.x;
-      const int rows_here = w.seq < 0 ? (a.n_tokens - w.first) * a.group : w.count * a.group;
-      const int rows = slot < a.n_partials ? min(min(kFewRows, a.rows_alloc), rows_here - w.r * kFewRows) : 0;
-      if (threadIdx.x < rows) {
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) top = fmaxf(top, stat[x][threadIdx.x].x);
-        if (top != -INFINITY)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sum += exp2_fast(stat[x][threadIdx.x].x - top) * stat[x][threadIdx.x].y;
-        a.ml[(long long)slot * a.rows_alloc + threadIdx.x] = make_float2(top, sum);
-      }
-#pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float(&v)[4] = o[half * 8 + i];
-          float* at = joined + (warp * 16 + g) * 64 + 8 * i + 2 * c;
-          *reinterpret_cast<float2*>(at) = make_float2(v[0] * f[0], v[1] * f[0]);
-          *reinterpret_cast<float2*>(at + 8 * 64) = make_float2(v[2] * f[1], v[3] * f[1]);
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t f[4];
+          const int row = ((lane >> 4) << 3) + (lane & 7), ch = 2 * k + ((lane >> 3) & 1);
+          ldmatrix4<false>(f, kb + row * (2 * D) + ((ch ^ (row & 7)) << 4));
+          Mma<T>::run(s[0], qf[k], f[0], f[1]);
+          Mma<T>::run(s[1], qf[k], f[2], f[3]);
         }
-        __syncthreads();
+        // scores in units of log 2; keys a row does not see get -inf
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = key + 8 * n + 2 * c + (e & 1);
+            s[n][e] = at < lim[e >> 1] ? s[n][e] * a.scale_log2 : -INFINITY;
+            top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+          }
+        float alpha[2], base[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int e = (i * kFewThreads + threadIdx.x) * 4, row = e >> 6, col = e & 63;
-          if (row < rows) {
-            float4 v = *reinterpret_cast<const float4*>(joined + e);
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+          const float now = fmaxf(m[i], top[i]);
+          base[i] = now == -INFINITY ? 0.f : now;
+          alpha[i] = exp2_fast(m[i] - base[i]);
+          m[i] = now;
+        }
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int x = 1; x < 4; ++x) {
-              const float4 y = *reinterpret_cast<const float4*>(joined + x * 1024 + e);
-              v.x += y.x;
-              v.y += y.y;
-              v.z += y.z;
-              v.w += y.w;
-            }
-            *reinterpret_cast<float4*>(a.part + ((long long)slot * a.rows_alloc + row) * D + half * 64 + col) = v;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[n][e] = exp2_fast(s[n][e] - base[e >> 1]);
+            sum[e >> 1] += s[n][e];
+          }
+        l[0] = l[0] * alpha[0] + sum[0];
+        l[1] = l[1] * alpha[1] + sum[1];
+        const uint32_t p[4] = {Mma<T>::pack(s[0][0], s[0][1]), Mma<T>::pack(s[0][2], s[0][3]),
+                               Mma<T>::pack(s[1][0], s[1][1]), Mma<T>::pack(s[1][2], s[1][3])};
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][0] *= alpha[0];
+            o[i][1] *= alpha[0];
+            o[i][2] *= alpha[1];
+            o[i][3] *= alpha[1];
           }
         }
-        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t f[4];
+          const int row = lane & 15, ch = 2 * d + (lane >> 4);
+          ldmatrix4<true>(f, vb + row * (2 * D) + ((ch ^ (row & 7)) << 4));
+          Mma<T>::run(o[2 * d], p, f[0], f[1]);
+          Mma<T>::run(o[2 * d + 1], p, f[2], f[3]);
+        }
       }
-      fresh = true;
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
-    if (left > 0) w.next(a, b);
-  }
+    // ---- join the four warps' partials and write the segment's
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (c == 0) stat[warp][g + 8 * i] = make_float2(m[i], l[i]);
+    }
+    __syncthreads();
+    float f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) top = fmaxf(top, stat[x][g + 8 * i].x);
+      f[i] = top == -INFINITY ? 0.f : exp2_fast(m[i] - top);
+    }
+    if (threadIdx.x < rows) {
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) top = fmaxf(top, stat[x][threadIdx.x].x);
+      if (top != -INFINITY)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sum += exp2_fast(stat[x][threadIdx.x].x - top) * stat[x][threadIdx.x].y;
+      a.ml[(long long)slot * a.rows_alloc + threadIdx.x] = make_float2(top, sum);
+    }
+#pragma unroll
+    for (int half = 0; half < D / 64; ++half) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float(&v)[4] = o[half * 8 + i];
+        float* at = joined + (warp * 16 + g) * 64 + 8 * i + 2 * c;
+        *reinterpret_cast<float2*>(at) = make_float2(v[0] * f[0], v[1] * f[0]);
+        *reinterpret_cast<float2*>(at + 8 * 64) = make_float2(v[2] * f[1], v[3] * f[1]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int e = (i * kFewThreads + threadIdx.x) * 4, row = e >> 6, col = e & 63;
+        if (row < rows) {
+          float4 v = *reinterpret_cast<const float4*>(joined + e);
+#pragma unroll
+          for (int x = 1; x < 4; ++x) {
+            const float4 y = *reinterpret_cast<const float4*>(joined + x * 1024 + e);
+            v.x += y.x;
+            v.y += y.y;
+            v.z += y.z;
+            v.w += y.w;
+          }
+          *reinterpret_cast<float4*>(a.part + ((long long)slot * a.rows_alloc + row) * D + half * 64 + col) = v;
+        }
+      }
+      __syncthreads();
+    }
+  } while (w.next(a, b));
   if (bad) atomicOr(a.status, bad);
 }
 
@@ -579,10 +648,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
 // group v % 2, and since the tensor core works in that order, S(v + 2) being
 // complete means that PV(v) is: no other barrier guards a group's scores or
 // its output.
-//   WIDE (more than 128 rows): the groups have different rows and share every
-//   K and V tile, which halves what has to come out of L2.
-//   else: the groups have the same rows and take every other key tile; each
-//   leaves a partial of its own (two `ways` a slot).
+//   wide segments (more than 128 rows): the groups have different rows and
+//   share every K and V tile, which halves what has to come out of L2;
+//   others: the groups have the same rows and take every other key tile.
+// Each group leaves a partial of its own, so a slot has two `ways`.
 // The running maximum is raised, and O rescaled in tensor memory, only when a
 // tile's maximum exceeds it by more than 8 (a factor 256, which the 16-bit
 // weights and fp32 sums hold without loss of precision), i.e. hardly ever after
@@ -685,6 +754,33 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// Two fp32 values in one 64-bit register: sm_100 adds and multiplies them in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float2 split(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int x, int row, int head, int page,
@@ -696,43 +792,10 @@ __device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int 
       : "memory");
 }
 
-// A block's part of one segment: key tiles t0 .. t1 - 1.
-template <int ROWS>
-struct Piece {
-  Walk<ROWS, kTile> w;
-  long long left;
-  int t0, t1;
-
-  __device__ __forceinline__ void begin(const AttendArgs& a, const Begin& b) {
-    left = b.u1 - b.u0;
-    w.start(a, b);
-    cut(a);
-  }
-  // Key tiles that no row of the tile sees are left out (a later part of a prompt's own keys).
-  __device__ __forceinline__ void cut(const AttendArgs& a) {
-    t0 = w.t;
-    t1 = (int)min((long long)w.kt, t0 + left);
-    left -= t1 - t0;
-    if (w.seq >= 0) {
-      const int last = min(w.r * ROWS + ROWS, w.count * a.group) - 1;
-      const int sees = min(w.len, w.before + last / a.group + 1);
-      t1 = max(t0, min(t1, (max(sees, 0) + kTile - 1) / kTile));
-    }
-  }
-  __device__ __forceinline__ bool next(const AttendArgs& a, const Begin& b) {
-    if (left <= 0) return false;
-    w.t = w.kt - 1;
-    w.next(a, b);
-    cut(a);
-    return true;
-  }
-};
-
-template <class T, int D, bool WIDE>
+template <class T, int D>
 __global__ void __launch_bounds__(kManyThreads, 1)
     many_rows_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
-  constexpr int ROWS = WIDE ? 2 * kTile : kTile;
   constexpr int R = kRing<D>, TB = kTileBytes<D>, HALF = kTile * 128;   // HALF: bytes of 64 columns of a tile
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (shared_addr(smem_raw) & 1023)) & 1023);
@@ -743,7 +806,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __shared__ long long plan_sm[28];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const Begin b = plan_block<kManyThreads, ROWS, kTile>(a, plan_sm);
+  const Begin b = plan_block<ManyCut, kManyThreads>(a, plan_sm);
   if (b.u0 >= b.u1) return;   // the whole block
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(shared_addr(&tmem_slot))
@@ -774,7 +837,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    Piece<ROWS> pc;
+    Piece<ManyCut> pc;
     pc.begin(a, b);
     if (warp == 8) {
       // ---- loads: lane i brings the i-th page of a tile
@@ -783,11 +846,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       do {
         for (int t = pc.t0; t < pc.t1; ++t, ++n) {
           const int key = t * kTile + lane * box;
-          const int held = min(kTile, pc.w.len - t * kTile);
+          const int held = min(kTile, pc.len - t * kTile);
           const int boxes = (held + box - 1) / box;
           int page = 0;
           if (lane < boxes) {
-            page = pc.w.row[key >> a.page_shift];
+            page = pc.table[key >> a.page_shift];
             if ((unsigned)page >= (unsigned)a.n_pages) {   // outside: the copy's fill, zeros
               page = a.n_pages;
               bad |= kStatusIndex;
@@ -807,7 +870,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   #pragma unroll
               for (int h = 0; h < D / 64; ++h)
                 tma_page(ring + slot * TB + h * HALF + lane * box * 128, kv ? &map_v : &map_k, 64 * h,
-                         key & ((1 << a.page_shift) - 1), pc.w.h, page, &full[slot]);
+                         key & ((1 << a.page_shift) - 1), pc.h, page, &full[slot]);
             }
           }
           if (dead) break;
@@ -818,13 +881,16 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     } else if (warp == 9) {
       // ---- products
       if (lane == 0) {
-        constexpr uint32_t qk = mma_shape<T>(kTile, kTile, false), pv = mma_shape<T>(kTile, D, true);
+        constexpr uint32_t pv = mma_shape<T>(kTile, D, true);
+        // a negative scale negates the queries, so that the softmax knows positive ones only
+        const uint32_t qk = mma_shape<T>(kTile, kTile, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
         uint32_t steps[2] = {0, 0}, pieces[2] = {0, 0};
         do {
-          const int tiles = pc.t1 - pc.t0, nv = WIDE ? 2 * tiles : tiles;
+          const bool wide = pc.rows_left() > kTile;
+          const int tiles = pc.t1 - pc.t0, nv = wide ? 2 * tiles : tiles;
           auto score = [&](int v) {   // S of step v
             const int g = v & 1;
-            const uint32_t x = 2 * (n + (WIDE ? v >> 1 : v));
+            const uint32_t x = 2 * (n + (wide ? v >> 1 : v));
             if (v < 2) {
               if (!dead && !mbar_wait(&q_full[g], pieces[g] & 1)) dead = true;
               ++pieces[g];
@@ -838,13 +904,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               mma_ss(tmem + 128 * g, tile_desc(q + off, 16, 1024), tile_desc(k + off, 16, 1024), qk, s > 0);
             }
             tc_commit(&s_full[g]);
-            if (!WIDE || g == 1) tc_commit(&empty[x % R]);
+            if (!wide || g == 1) tc_commit(&empty[x % R]);
           };
           if (nv > 0) score(0);
           if (nv > 1) score(1);
           for (int v = 0; v < nv; ++v) {
             const int g = v & 1;
-            const uint32_t x = 2 * (n + (WIDE ? v >> 1 : v)) + 1;
+            const uint32_t x = 2 * (n + (wide ? v >> 1 : v)) + 1;
             if (!dead && !mbar_wait(&p_full[g], steps[g] & 1)) dead = true;
             ++steps[g];
             if (!dead && !mbar_wait(&full[x % R], (x / R) & 1)) dead = true;
@@ -854,7 +920,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             for (int s = 0; s < kTile / 16; ++s)
               mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * s, tile_desc(vt + s * 2048, HALF, 1024), pv,
                      v >= 2 || s > 0);
-            if (!WIDE || g == 1) tc_commit(&empty[x % R]);
+            if (!wide || g == 1) tc_commit(&empty[x % R]);
             if (v + 2 < nv) score(v + 2);
             else tc_commit(&o_full[g]);
           }
@@ -864,39 +930,51 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    Piece<ROWS> pc;
+    Piece<ManyCut> pc;
     pc.begin(a, b);
     // ---- softmax group g, this thread's row
     const int g = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + 128 * g + lane0, to = tmem + 256 + 128 * g + lane0;
     const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);   // above 0, so that -inf stays -inf
-    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;   // a negative scale turns the queries' signs
     uint32_t steps = 0, pieces = 0;
+    auto steps_of = [&](const Piece<ManyCut>& x) {   // of this group
+      const int tiles = x.t1 - x.t0;
+      return x.rows_left() > kTile ? tiles : (tiles - g + 1) / 2;
+    };
+    auto row_of = [&](const Piece<ManyCut>& x) {     // of this thread, among the key set's
+      return x.r * ManyCut::kRows + (x.rows_left() > kTile ? g * kTile : 0) + row;
+    };
+    // The group's queries for a piece, under way: the products that read the last ones are done by then.
+    auto load_queries = [&](const Piece<ManyCut>& x) {
+      if (steps_of(x) > 0) {
+        const int at = row_of(x), tok = at / a.group;
+        const bool in = at < x.rows;
+        const unsigned char* src =
+            in ? a.q + (long long)(x.first + tok) * a.q_token + (long long)(x.h * a.group + at - tok * a.group) * a.q_head
+               : a.q;
+        const uint32_t dst = shared_addr(qs + g * TB) + row * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          copy16(dst + (c >> 3) * HALF + (((c & 7) ^ (row & 7)) << 4), src + (in ? 16 * c : 0), in ? 16 : 0);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load_queries(pc);
+    bool more = true;
     do {
-      const int tiles = pc.t1 - pc.t0;
-      const int mine = WIDE ? tiles : (tiles - g + 1) / 2;   // steps of this group
-      const int at = pc.w.r * ROWS + (WIDE ? g * kTile : 0) + row;
-      const int tok = at / a.group;
-      const bool in = (pc.w.seq < 0 || tok < pc.w.count) && pc.w.first + tok < a.n_tokens;
-      const int lim = in ? (pc.w.seq < 0 ? pc.w.len : min(pc.w.len, pc.w.before + tok + 1)) : 0;
+      const int tiles = pc.t1 - pc.t0, mine = steps_of(pc);
+      const bool wide = pc.rows_left() > kTile;
+      const int at = row_of(pc);
+      const int lim = at < pc.rows ? pc.sees(at / a.group) : 0;
       float m = -INFINITY, l = 0.f;
       if (mine > 0) {
-        // the group's queries (their last readers, the products of the piece before, are done: o_full)
-        const unsigned char* src =
-            a.q + (long long)(pc.w.first + tok) * a.q_token + (long long)(pc.w.h * a.group + at - tok * a.group) * a.q_head;
-        unsigned char* dst = qs + g * TB + row * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 x = in ? *reinterpret_cast<const uint4*>(src + 16 * c) : make_uint4(0, 0, 0, 0);
-          x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * HALF + (((c & 7) ^ (row & 7)) << 4)) = x;
-        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         async_fence();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[g]);
         for (int j = 0; j < mine; ++j, ++steps) {
-          const int tile = WIDE ? j : 2 * j + g;
+          const int tile = wide ? j : 2 * j + g;
           const int key = (pc.t0 + tile) * kTile;
           if (!dead && !mbar_wait(&s_full[g], steps & 1)) dead = true;
           dead = __any_sync(0xffffffffu, dead);
@@ -911,10 +989,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             for (int i = 0; i < kTile; ++i)
               if (key + i >= lim) s[i] = 0xff800000u;   // -inf
           }
-          float top = -INFINITY;
+          // four chains each, so that their latency is covered with two warps a scheduler
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) top = fmaxf(top, __uint_as_float(s[i]));
-          top *= scale;
+          for (int i = 0; i < kTile; i += 8)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tops[c] = max3(tops[c], __uint_as_float(s[i + 2 * c]), __uint_as_float(s[i + 2 * c + 1]));
+          const float top = scale * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
           const bool raise = top > m + kRaise;
           if (__any_sync(0xffffffffu, raise)) {
             const float f = raise ? exp2_fast(m - top) : 1.f;
@@ -933,24 +1015,24 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
-          float sum = 0.f;
+          const uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
+          uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) {
-            const float p = exp2_fast(fmaf(__uint_as_float(s[i]), scale, -base));
-            sum += p;
-            s[i] = __float_as_uint(p);
+          for (int i = 0; i < kTile / 2; ++i) {
+            const float2 x = split(fma2(pair(s[2 * i], s[2 * i + 1]), scale2, base2));
+            const float p = exp2_fast(x.x), q = exp2_fast(x.y);
+            sums[i & 3] = add2(sums[i & 3], pair(p, q));
+            s[i] = Mma<T>::pack(p, q);
           }
-          l += sum;
-#pragma unroll
-          for (int i = 0; i < kTile / 2; ++i)
-            s[i] = Mma<T>::pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+          const float2 sum = split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+          l += sum.x + sum.y;
           tmem_store32(ts, s);
           tmem_store32(ts + 32, s + 32);
           tmem_store_wait();
-          if (pc.w.len - key < kTile && (!WIDE || g == 0)) {   // V rows past the end
+          if (pc.len - key < kTile && (!wide || g == 0)) {   // V rows past the end
             const uint32_t x = 2 * (n + tile) + 1;
             if (!dead && !mbar_wait(&full[x % R], (x / R) & 1)) dead = true;
-            if (row >= pc.w.len - key) {
+            if (row >= pc.len - key) {
 #pragma unroll
               for (int c = 0; c < D / 8; ++c)
                 *reinterpret_cast<uint4*>(ring + x % R * TB + (c >> 3) * HALF + row * 128 + (c & 7) * 16) =
@@ -963,19 +1045,22 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[g]);
         }
+      }
+      Piece<ManyCut> nx = pc;
+      more = nx.next(a, b);
+      if (more) load_queries(nx);
+      if (mine > 0) {
         if (!dead && !mbar_wait(&o_full[g], pieces & 1)) dead = true;
         dead = __any_sync(0xffffffffu, dead);
         ++pieces;
         tc_after();
       }
-      // ---- the partial
-      const int rows_here = pc.w.seq < 0 ? (a.n_tokens - pc.w.first) * a.group : pc.w.count * a.group;
-      const long long slot = (pc.w.seg + (int)blockIdx.x) * (WIDE ? 1ll : 2ll) + (WIDE ? 0 : g);
-      const int r = (WIDE ? g * kTile : 0) + row;
-      const bool keep = at < rows_here && r < a.rows_alloc && slot < a.n_partials;
-      if (keep) a.ml[slot * a.rows_alloc + r] = make_float2(m, l);
+      // ---- the partial: rows of one way, or two ways of the same rows
+      const long long slot = (pc.seg + (long long)blockIdx.x) * 2 + g;
+      const bool keep = at < pc.rows && row < a.rows_alloc && slot < a.n_partials;
+      if (keep) a.ml[slot * a.rows_alloc + row] = make_float2(m, l);
       if (mine > 0) {
-        float* dst = a.part + (slot * a.rows_alloc + r) * D;
+        float* dst = a.part + (slot * a.rows_alloc + row) * D;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -989,7 +1074,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         tc_before();
       }
       n += tiles;
-    } while (!dead && pc.next(a, b));
+      pc = nx;
+    } while (!dead && more);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   if (dead) bad |= lb::kStatusTimeout;
   if (bad) atomicOr(a.status, bad);
@@ -1010,11 +1097,12 @@ struct Source {
   const SeqPlan* seqs;
   const float2* ml;
   const float* part;
-  int rows, rows_alloc, blocks, n_partials;   // query rows of a tile; blocks of the launch
-  int ways;                                   // partials of a slot
+  int few;                    // of few_rows_kernel, else of many_rows_kernel
+  int ways;                   // partials of a slot
+  int rows_alloc, n_partials;
 };
 struct JoinArgs {
-  Source prefix, own;   // head null: no such key set
+  Source prefix, own;   // prefix.head null: no prefix
   unsigned char* out;
   long long out_token, out_head;   // bytes
   int n, n_tokens, heads, group;
@@ -1041,43 +1129,68 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   const int kv = h / a.group, sub = h - kv * a.group;
   float acc[E] = {}, m = -INFINITY, l = 0.f;
 
-  auto add = [&](const Source& S, int seg, long long ua, int kt, int row) {
-    if (kt <= 0) return;
-    const long long U = S.head->units, G = min((long long)S.blocks, U);
-    const int c0 = (int)(((ua + 1) * G - 1) / U), c1 = (int)(((ua + kt) * G - 1) / U);
-    for (int x = (seg + c0) * S.ways; x < (seg + c1 + 1) * S.ways; ++x) {
-      const long long at = (long long)x * S.rows_alloc + row;
-      if (x >= S.n_partials) continue;
-      const float2 p = S.ml[at];
-      if (p.x == -INFINITY) continue;   // nothing seen; its output row need not have been written
-      float v[E];
-      if constexpr (E == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(S.part + at * D + lane * 4);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(S.part + at * D + lane * 2);
-        v[0] = x.x, v[1] = x.y;
-      }
-      const float now = fmaxf(m, p.x);
-      const float f0 = exp2_fast(m - now), f1 = exp2_fast(p.x - now);
-      m = now;
-      l = l * f0 + p.y * f1;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
+  // the partials of one segment (units ua .. ua + ext - 1), ways w0 .. w1 - 1 of each slot, row `row` of them
+  auto add = [&](const Source& S, int seg, long long ua, int ext, int w0, int w1, int row) {
+    if (ext <= 0) return;
+    const long long W = S.head->width, ub = ua + ext - 1;
+    int c0, c1;
+    if ((ub | W) >> 32 == 0) {   // nearly always: two divisions of 32 bits
+      c0 = (int)((uint32_t)ua / (uint32_t)W);
+      c1 = (int)((uint32_t)ub / (uint32_t)W);
+    } else {
+      c0 = (int)(ua / W);
+      c1 = (int)(ub / W);
     }
+    for (int c = c0; c <= c1; ++c)
+      for (int way = w0; way < w1; ++way) {
+        const long long x = (seg + (long long)c) * S.ways + way, at = x * S.rows_alloc + row;
+        if (x >= S.n_partials) continue;
+        const float2 p = S.ml[at];
+        if (p.x == -INFINITY) continue;   // nothing seen; its output row need not have been written
+        float v[E];
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(S.part + at * D + lane * 4);
+          v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(S.part + at * D + lane * 2);
+          v[0] = y.x, v[1] = y.y;
+        }
+        const float now = fmaxf(m, p.x);
+        const float f0 = exp2_fast(m - now), f1 = exp2_fast(p.x - now);
+        m = now;
+        l = l * f0 + p.y * f1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
+      }
+  };
+  auto prefix_set = [&](auto cut) {
+    using C = decltype(cut);
+    const PlanHead H = *a.prefix.head;
+    const int row = (t - H.t0) * a.group + sub, r = row / C::kRows, in = row - r * C::kRows;
+    const int left = H.p_rows - r * C::kRows;
+    const bool wide = C::cost(left) > 1;
+    add(a.prefix, kv * H.p_rt + r, (long long)kv * H.p_head + (long long)r * extent<C>(H.p_kt, C::kRows),
+        extent<C>(H.p_kt, left), wide ? in >> 7 : 0, wide ? (in >> 7) + 1 : a.prefix.ways, wide ? in & 127 : in);
+  };
+  auto own_set = [&](auto cut) {
+    using C = decltype(cut);
+    const SeqPlan s = a.own.seqs[seq];
+    const int row = (t - s.first) * a.group + sub, r = row / C::kRows, in = row - r * C::kRows;
+    const int left = s.count * a.group - r * C::kRows;
+    const bool wide = C::cost(left) > 1;
+    int before = 0;   // units of the head's row tiles before this one
+    for (int i = lane; i < r; i += 32) before += own_extent<C>(s.count, a.group, s.len, s.before, i);
+    before = __reduce_add_sync(0xffffffffu, before);
+    add(a.own, s.segs_before + kv * row_tiles<C>(s.count * a.group) + r,
+        s.units_before + (long long)kv * s.head + before, own_extent<C>(s.count, a.group, s.len, s.before, r),
+        wide ? in >> 7 : 0, wide ? (in >> 7) + 1 : a.own.ways, wide ? in & 127 : in);
   };
   if (a.prefix.head) {
-    const PlanHead H = *a.prefix.head;
-    const int row = (t - H.t0) * a.group + sub;
-    const int seg = kv * H.p_rt + row / a.prefix.rows;
-    add(a.prefix, seg, (long long)seg * H.p_kt, H.p_kt, row % a.prefix.rows);
+    if (a.prefix.few) prefix_set(FewCut{});
+    else prefix_set(ManyCut{});
   }
-  if (a.own.head) {
-    const SeqPlan s = a.own.seqs[seq];
-    const int row = (t - s.first) * a.group + sub;
-    const int k = kv * s.rt + row / a.own.rows;
-    add(a.own, s.segs_before + k, s.units_before + (long long)k * s.kt, s.kt, row % a.own.rows);
-  }
+  if (a.own.few) own_set(FewCut{});
+  else own_set(ManyCut{});
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
   T r[E];
 #pragma unroll
@@ -1104,15 +1217,14 @@ size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 // Work memory of one launch: [head][sequences][ml][partials].
 struct Region {
-  int blocks, rows, rows_alloc, ways;   // rows: query rows of a tile; 0: no such launch
+  int blocks, rows_alloc, ways;   // blocks 0: no such launch
   long long partials;
   size_t seqs, ml, part, bytes;
 };
-Region region(int rows, int ways, int blocks, int64_t segs, int64_t most_rows, int n, int D) {
+Region region(int way_rows, int ways, int blocks, int64_t segs, int64_t most_rows, int n, int D) {
   Region g;
   g.blocks = blocks;
-  g.rows = rows;
-  g.rows_alloc = (int)std::min<int64_t>(rows, most_rows);
+  g.rows_alloc = (int)std::min<int64_t>(way_rows, most_rows);
   g.ways = ways;
   g.partials = (segs + blocks) * ways;
   g.seqs = up(sizeof(PlanHead));
@@ -1125,7 +1237,7 @@ Region region(int rows, int ways, int blocks, int64_t segs, int64_t most_rows, i
 // Which launch takes what.  The rows that read a key set decide: up to 16 go
 // to the few-rows kernel (its one tile), more to the many-rows kernel.
 struct Split {
-  bool few_prefix, few_own, many_prefix, many_own, wide;
+  bool few_prefix, few_own, many_prefix, many_own;
   Region few, many;
 };
 Split split_of(int heads, int group, int n_tokens, int n, int most_q, bool with_prefix, int D) {
@@ -1146,9 +1258,7 @@ Split split_of(int heads, int group, int n_tokens, int n, int most_q, bool with_
                    std::max(s.few_prefix ? p_rows : 0, s.few_own ? o_rows : 0), n, D);
   if (s.many_prefix || s.many_own) {
     const int64_t most = std::max(s.many_prefix ? p_rows : 0, s.many_own ? o_rows : 0);
-    s.wide = most > kTile;
-    const int rows = s.wide ? 2 * kTile : kTile;
-    s.many = region(rows, s.wide ? 1 : 2, sm_count(), segs(rows, s.many_prefix, s.many_own), most, n, D);
+    s.many = region(kTile, 2, sm_count(), segs(ManyCut::kRows, s.many_prefix, s.many_own), most, n, D);
   }
   return s;
 }
@@ -1195,26 +1305,19 @@ lb_status plane_map(const lb_cache& c, const lb_plane& P, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? LB_OK : LB_ERR_SHAPE;   // strides that the copy engine does not take
 }
 
-template <class T, int D, bool WIDE>
-cudaError_t launch_many(const AttendArgs& a, int blocks, const CUtensorMap& k, const CUtensorMap& v,
-                        cudaStream_t st) {
-  static lb::PerDevice smem;
-  const cudaError_t e = allow_smem(many_rows_kernel<T, D, WIDE>, smem, kManySmem<D>);
-  if (e != cudaSuccess) return e;
-  many_rows_kernel<T, D, WIDE><<<blocks, kManyThreads, kManySmem<D>, st>>>(a, k, v);
-  return cudaGetLastError();
-}
-
 template <class T, int D>
 cudaError_t launch(const Split& s, const AttendArgs& few, const AttendArgs& many, const CUtensorMap& k,
                    const CUtensorMap& v, const JoinArgs& join, cudaStream_t st) {
+  static lb::PerDevice few_smem, many_smem;
   cudaError_t e = cudaSuccess;
-  if (s.many.rows)
-    e = s.wide ? launch_many<T, D, true>(many, s.many.blocks, k, v, st)
-               : launch_many<T, D, false>(many, s.many.blocks, k, v, st);
-  if (e == cudaSuccess && s.few.rows) {
-    static lb::PerDevice smem;
-    e = allow_smem(few_rows_kernel<T, D>, smem, kFewSmem<D>);
+  if (s.many.blocks) {
+    e = allow_smem(many_rows_kernel<T, D>, many_smem, kManySmem<D>);
+    if (e != cudaSuccess) return e;
+    many_rows_kernel<T, D><<<s.many.blocks, kManyThreads, kManySmem<D>, st>>>(many, k, v);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && s.few.blocks) {
+    e = allow_smem(few_rows_kernel<T, D>, few_smem, kFewSmem<D>);
     if (e != cudaSuccess) return e;
     few_rows_kernel<T, D><<<s.few.blocks, kFewThreads, kFewSmem<D>, st>>>(few);
     e = cudaGetLastError();
@@ -1271,7 +1374,7 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   if (work_bytes < s.few.bytes + s.many.bytes) return LB_ERR_SHAPE;
   if (s.few.partials > INT32_MAX || s.many.partials > INT32_MAX) return LB_ERR_SHAPE;
   CUtensorMap map_k{}, map_v{};
-  if (s.many.rows && ((r = plane_map(*c, K, &map_k)) != LB_OK || (r = plane_map(*c, V, &map_v)) != LB_OK)) return r;
+  if (s.many.blocks && ((r = plane_map(*c, K, &map_k)) != LB_OK || (r = plane_map(*c, V, &map_v)) != LB_OK)) return r;
   unsigned* status = nullptr;
   cudaError_t e = lb::touch_cache_status(&status);
   if (e != cudaSuccess) return lb::cuda_fail(e);
@@ -1310,7 +1413,7 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
     x.part = reinterpret_cast<float*>(w + g.part);
     x.rows_alloc = g.rows_alloc;
     x.n_partials = (int)g.partials;
-    const Source src{x.head, x.seqs, x.ml, x.part, g.rows, g.rows_alloc, g.blocks, (int)g.partials, g.ways};
+    const Source src{x.head, x.seqs, x.ml, x.part, g.ways == 1, g.ways, g.rows_alloc, (int)g.partials};
     if (own) j.own = src;
     if (with_prefix) j.prefix = src;
     return x;
