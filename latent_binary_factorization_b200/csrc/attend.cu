@@ -34,15 +34,20 @@ namespace {
 constexpr unsigned kStatusIndex = 1u << LB_ERR_INDEX;
 
 // How a kernel cuts its segments: query rows of a tile, keys of a tile, units
-// that a segment's beginning and end are worth, units of one key tile.
+// that a segment's beginning and end are worth, units of one key tile.  A wide
+// row tile, of more than 128 rows, costs two (see many_rows_kernel).
 struct FewCut {
   static constexpr int kRows = 16, kKeys = 64, kSetup = 1;
-  static __device__ __forceinline__ int cost(int) { return 1; }
 };
 struct ManyCut {
-  static constexpr int kRows = 256, kKeys = 128, kSetup = 3;
-  // up to 128 rows take half of the products (see many_rows_kernel)
-  static __device__ __forceinline__ int cost(int rows) { return rows > 128 ? 2 : 1; }
+  static constexpr int kRows = 256, kKeys = 128, kSetup = 4;
+};
+constexpr int kMaxUnits = 0x7fffffff;
+
+// Division by a number fixed at launch, exact for 0 <= n < 2^31.
+struct Divisor {
+  unsigned mul, shift;
+  __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi(mul, (unsigned)n) + (unsigned)n) >> shift); }
 };
 
 // A plane of one cache, strides in bytes.
@@ -53,17 +58,19 @@ struct PlaneArg {
 
 // What both the partial kernels and the join know of a launch.
 struct PlanHead {
-  long long width;          // units of a block
+  int width;                // units of a block; 0: more units than can be counted, nothing is done
   int t0, t1;               // tokens of the batch
   int p_rows, p_rt, p_kt;   // prefix: query rows, row tiles a head, key tiles
   int p_head;               // units of one head's segments
+  int pad;
 };
 struct SeqPlan {
-  long long units_before;   // units of the launch before this sequence's (the prefix's included)
-  int segs_before;          // segments before this sequence's (the prefix's included)
-  int first, count;         // tokens
-  int len, before;          // see Seq
-  int head;                 // units of one head's segments
+  int units_before;   // units of the launch before this sequence's (the prefix's included)
+  int segs_before;    // segments before this sequence's (the prefix's included)
+  int first, count;   // tokens
+  int len, before;    // see Seq
+  int head;           // units of one head's segments
+  int pad;
 };
 
 struct AttendArgs {
@@ -78,6 +85,7 @@ struct AttendArgs {
   const int* starts;
   int n, n_tokens, prefix, most_q;
   int heads, group;            // K and V heads; query heads of each
+  Divisor by_group;
   float scale_log2;
   int do_prefix, do_own;       // which key sets this launch takes
   PlanHead* head;              // written by block 0 for the join
@@ -113,106 +121,111 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int i) {
   s.first = min(max(a.starts[i], 0), a.n_tokens);
   const int end = min(max(a.starts[i + 1], s.first), a.n_tokens);
   const bool ok = s.slot >= 0 && s.slot < a.n_slots;
-  const long long cap = (long long)a.max_pages << a.page_shift;
-  s.len = ok ? (int)min((long long)max(a.length[s.slot], 0), cap) : 0;
+  s.len = ok ? min(max(a.length[s.slot], 0), a.max_pages << a.page_shift) : 0;
   s.before = s.len - (end - s.first);
   s.count = min(end - s.first, a.most_q);
   return s;
 }
 
+__device__ __forceinline__ int up_div(int a, int b) { return (a + b - 1) / b; }   // b: a constant; a + b fits (cap)
+
+// Key tiles that row tile r of a sequence sees any key of.
 template <class C>
-__device__ __forceinline__ int row_tiles(int rows) {
-  return (rows + C::kRows - 1) / C::kRows;
+__device__ __forceinline__ int own_tiles(const Divisor& by_group, int rows, int len, int before, int r) {
+  const int last = by_group(min((r + 1) * C::kRows, rows) - 1);
+  return up_div(min(len, max(before + last + 1, 0)), C::kKeys);
 }
-// Key tiles that row tile r of a sequence sees any key of, and its segment's extent.
-template <class C>
-__device__ __forceinline__ int own_tiles(int count, int group, int len, int before, int r) {
-  const int last = (min((r + 1) * C::kRows, count * group) - 1) / group;
-  const int sees = min(len, max(before + last + 1, 0));
-  return (int)(((long long)sees + C::kKeys - 1) / C::kKeys);
-}
+// A segment's extent.
 template <class C>
 __device__ __forceinline__ int extent(int tiles, int rows_left) {
-  return tiles ? C::kSetup + tiles * C::cost(rows_left) : 0;
-}
-template <class C>
-__device__ __forceinline__ int own_extent(int count, int group, int len, int before, int r) {
-  return extent<C>(own_tiles<C>(count, group, len, before, r), count * group - r * C::kRows);
+  return tiles ? C::kSetup + (rows_left > 128 ? 2 * tiles : tiles) : 0;
 }
 // Units of one head's segments of a sequence.
 template <class C>
-__device__ __forceinline__ int own_head(int count, int group, int len, int before) {
-  int sum = 0;
-  for (int r = 0, n = row_tiles<C>(count * group); r < n; ++r) sum += own_extent<C>(count, group, len, before, r);
-  return sum;
+__device__ __forceinline__ int own_head(const Divisor& by_group, int rows, int len, int before) {
+  unsigned sum = 0;   // an extent is below 2^19: the cap below is reached before the sum wraps
+#pragma unroll 1
+  for (int r = 0; r * C::kRows < rows && sum < kMaxUnits; ++r)
+    sum += extent<C>(own_tiles<C>(by_group, rows, len, before, r), rows - r * C::kRows);
+  return (int)min(sum, (unsigned)kMaxUnits);
 }
 
 // Where a block begins.
 struct Begin {
-  long long u0, u1;          // its units
+  int u0, u1;                // its units
   int p_rt, p_kt, p_rows, p_head, p_len, t0;
   int seq;                   // sequence of u0; -1: the prefix
-  long long seq_u;           // units before it
+  int seq_u;                 // units before it
   int seq_segs;              // segments before it
 };
 
-// Run by the whole block (THREADS threads).  Two sweeps over the sequences,
-// THREADS at a time: the total, then the place of u0.  Block 0 leaves the
-// plan for join_kernel.
+// Run by the whole block (THREADS threads).  Two sweeps over the
+// sequences, THREADS at a time: the total, then the place of u0.  Block 0
+// leaves the plan for join_kernel.
 template <class C, int THREADS>
-__device__ __forceinline__ Begin plan_block(const AttendArgs& a, long long* sm /* THREADS / 32 * 2 + 3 */) {
+__device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Begin b;
   b.t0 = min(max(a.starts[0], 0), a.n_tokens);
   const int t1 = min(max(a.starts[a.n], b.t0), a.n_tokens);
-  b.p_rows = b.p_rt = b.p_kt = b.p_len = b.p_head = 0;
+  b.p_rows = b.p_rt = b.p_kt = b.p_len = 0;
+  long long p_units = 0;   // the sums are taken in 64 bits, and used if they fit 31
   if (a.do_prefix) {
-    const long long cap = (long long)a.max_pages << a.page_shift;
-    b.p_len = (int)min((long long)max(a.length[a.prefix], 0), cap);
+    b.p_len = min(max(a.length[a.prefix], 0), a.max_pages << a.page_shift);
     b.p_rows = (t1 - b.t0) * a.group;
-    b.p_rt = row_tiles<C>(b.p_rows);
-    b.p_kt = (int)(((long long)b.p_len + C::kKeys - 1) / C::kKeys);
+    b.p_rt = up_div(b.p_rows, C::kRows);
+    b.p_kt = up_div(b.p_len, C::kKeys);
     if (b.p_rt)
-      b.p_head = (b.p_rt - 1) * extent<C>(b.p_kt, C::kRows) + extent<C>(b.p_kt, b.p_rows - (b.p_rt - 1) * C::kRows);
+      p_units = (b.p_rt - 1ll) * extent<C>(b.p_kt, C::kRows) + extent<C>(b.p_kt, b.p_rows - (b.p_rt - 1) * C::kRows);
   }
-  const long long p_units = (long long)b.p_head * a.heads;
-  const long long p_segs = (long long)b.p_rt * a.heads;
-  long long* warp_u = sm;
-  long long* warp_s = sm + W;
-  long long* found = sm + 2 * W;   // sequence, units before, segments before
+  b.p_head = (int)min(p_units, (long long)kMaxUnits);
+  p_units *= a.heads;
+  const int p_segs = b.p_rt * a.heads;
+  __shared__ long long warp_u[W];
+  __shared__ int warp_s[W], found[3];   // sequence, units before, segments before
   long long total = p_units;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1) {
       // every block but the last ones has the same number of units; a block inside a segment always has some
-      const long long width = max((total + gridDim.x - 1) / gridDim.x, 1ll);
-      b.u0 = min(width * blockIdx.x, total);
-      b.u1 = min(width * (blockIdx.x + 1), total);
+      const bool fits = total <= kMaxUnits - 1024 * 1024;
+      const int width = fits ? max(((int)total + (int)gridDim.x - 1) / (int)gridDim.x, 1) : 0;
+      b.u0 = (int)min((long long)width * blockIdx.x, total);
+      b.u1 = (int)min((long long)width * (blockIdx.x + 1), total);
       b.seq = -1;
       b.seq_u = 0;
       b.seq_segs = 0;
-      if (blockIdx.x == 0 && tid == 0) *a.head = PlanHead{width, b.t0, t1, b.p_rows, b.p_rt, b.p_kt, b.p_head};
+      if (blockIdx.x == 0 && tid == 0) {
+        *a.head = PlanHead{width, b.t0, t1, b.p_rows, b.p_rt, b.p_kt, b.p_head, 0};
+        if (!fits) atomicOr(a.status, kStatusIndex);
+      }
       if (b.u0 < p_units || b.u0 >= b.u1) break;
     }
     long long u = p_units;
-    long long segs = p_segs;
+    int segs = p_segs;
     if (a.do_own)
+#pragma unroll 1
       for (int i0 = 0; i0 < a.n; i0 += THREADS) {
         const int i = i0 + tid;
-        int head = 0, rt = 0;
+        long long mine = 0;
+        int mine_s = 0, head = 0;
         Seq s{};
         if (i < a.n) {
           s = load_seq(a, i);
-          rt = row_tiles<C>(s.count * a.group);
-          head = own_head<C>(s.count, a.group, s.len, s.before);
+          const int rows = s.count * a.group;
+          mine_s = up_div(rows, C::kRows) * a.heads;
+          head = own_head<C>(a.by_group, rows, s.len, s.before);
+          mine = (long long)head * a.heads;
           if (s.slot != -1 && (s.slot < 0 || s.slot >= a.n_slots) && blockIdx.x == 0)
             atomicOr(a.status, kStatusIndex);
         }
-        const long long mine = (long long)head * a.heads, mine_s = (long long)rt * a.heads;
-        long long xu = mine, xs = mine_s;
-#pragma unroll
+        long long xu = mine;
+        int xs = mine_s;
+#pragma unroll 1
         for (int d = 1; d < 32; d <<= 1) {
-          const long long yu = __shfl_up_sync(0xffffffffu, xu, d), ys = __shfl_up_sync(0xffffffffu, xs, d);
+          const long long yu = __shfl_up_sync(0xffffffffu, xu, d);
+          const int ys = __shfl_up_sync(0xffffffffu, xs, d);
           if (lane >= d) {
             xu += yu;
             xs += ys;
@@ -224,7 +237,9 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a, long long* sm /
           warp_s[warp] = xs;
         }
         __syncthreads();
-        long long before_u = u + xu - mine, before_s = segs + xs - mine_s;
+        long long before_u = u + xu - mine;
+        int before_s = segs + xs - mine_s;
+#pragma unroll 1
         for (int w = 0; w < W; ++w) {
           if (w < warp) {
             before_u += warp_u[w];
@@ -235,19 +250,19 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a, long long* sm /
         }
         if (pass == 0) {
           if (blockIdx.x == 0 && i < a.n)
-            a.seqs[i] = SeqPlan{before_u, (int)before_s, s.first, s.count, s.len, s.before, head};
-        } else if (i < a.n && b.u0 >= before_u && b.u0 < before_u + mine) {
+            a.seqs[i] = SeqPlan{(int)min(before_u, (long long)kMaxUnits), before_s, s.first, s.count, s.len, s.before, head, 0};
+        } else if (b.u0 >= before_u && b.u0 < before_u + mine) {
           found[0] = i;
-          found[1] = before_u;
+          found[1] = (int)before_u;
           found[2] = before_s;
         }
       }
     total = u;
     if (pass == 1) {
       __syncthreads();
-      b.seq = (int)found[0];
+      b.seq = found[0];
       b.seq_u = found[1];
-      b.seq_segs = (int)found[2];
+      b.seq_segs = found[2];
     }
   }
   return b;
@@ -259,92 +274,93 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a, long long* sm /
 template <class C>
 struct Piece {
   int seq;                   // -1: the prefix
-  int h, r, rt;              // head, row tile, row tiles a head
+  int h, r;                  // head, row tile
   int seg;                   // segment number
   int rows;                  // query rows of the key set
   int first, len, before;    // first token; keys; keys before the first token
-  int kt;                    // key tiles of the segment
   const int* table;          // page table row
   int t0, t1;
-  long long left;            // units of the block still to come
+  int left;                  // units of the block still to come
 
   __device__ __forceinline__ int rows_left() const { return rows - r * C::kRows; }
   // Keys that token `tok` of the key set sees.
   __device__ __forceinline__ int sees(int tok) const { return seq < 0 ? len : min(len, before + tok + 1); }
 
-  __device__ __forceinline__ void enter(const AttendArgs& a, const Begin& b) {
+  __device__ __forceinline__ void enter(const AttendArgs& a) {
+    const Seq s = load_seq(a, seq);
+    rows = s.count * a.group;
+    first = s.first;
+    len = s.len;
+    before = s.before;
+    table = a.table + s.slot * a.table_stride;
+  }
+  __device__ __forceinline__ int ext(const AttendArgs& a) const {
+    return extent<C>(seq < 0 ? up_div(len, C::kKeys) : own_tiles<C>(a.by_group, rows, len, before, r), rows_left());
+  }
+  // Units x .. e - 1 of the segment, as far as they are this block's.
+  __device__ __forceinline__ void cut(int x, int e) {
+    const int n = min(e - x, left), wide = rows_left() > 128;
+    left -= n;
+    t0 = max(x - C::kSetup + wide, 0) >> wide;
+    t1 = max(x + n - C::kSetup + wide, 0) >> wide;
+  }
+  __device__ __forceinline__ void begin(const AttendArgs& a, const Begin& b) {
+    left = b.u1 - b.u0;
+    seq = b.seq;
+    int head = b.p_head;
     if (seq < 0) {
-      rt = b.p_rt;
       rows = b.p_rows;
       first = b.t0;
       len = before = b.p_len;
       table = a.table + a.prefix * a.table_stride;
     } else {
-      const Seq s = load_seq(a, seq);
-      rows = s.count * a.group;
-      rt = row_tiles<C>(rows);
-      first = s.first;
-      len = s.len;
-      before = s.before;
-      table = a.table + s.slot * a.table_stride;
+      enter(a);
+      head = own_head<C>(a.by_group, rows, len, before);
     }
-  }
-  __device__ __forceinline__ int tile(const AttendArgs& a, const Begin& b) {   // the extent
-    kt = seq < 0 ? b.p_kt : own_tiles<C>(rows / a.group, a.group, len, before, r);
-    return extent<C>(kt, rows_left());
-  }
-  // Units x .. ext - 1 of the segment, as far as they are this block's.
-  __device__ __forceinline__ void cut(int x, int ext) {
-    const int n = (int)min((long long)(ext - x), left);
-    left -= n;
-    const int c = C::cost(rows_left());
-    t0 = max(x - C::kSetup + c - 1, 0) / c;
-    t1 = max(x + n - C::kSetup + c - 1, 0) / c;
-  }
-  __device__ __forceinline__ void begin(const AttendArgs& a, const Begin& b) {
-    left = b.u1 - b.u0;
-    seq = b.seq;
-    enter(a, b);
-    const long long off = b.u0 - b.seq_u;
-    const int head = seq < 0 ? b.p_head : own_head<C>(rows / a.group, a.group, len, before);
-    h = (int)(off / max(head, 1));
-    int x = (int)(off - (long long)h * head);
+    int x = b.u0 - b.seq_u;
+    h = x / max(head, 1);
+    x -= h * head;
+    const int rt = up_div(rows, C::kRows);
     r = 0;
     if (seq < 0) {
       const int e = extent<C>(b.p_kt, C::kRows);
-      r = min(x / e, rt - 1);
+      r = min(x / max(e, 1), rt - 1);
       x -= r * e;
     }
-    int ext = tile(a, b);
-    while (x >= ext && r + 1 < rt) {
-      x -= ext;
+    int e = ext(a);
+#pragma unroll 1
+    while (x >= e && r + 1 < rt) {
+      x -= e;
       ++r;
-      ext = tile(a, b);
+      e = ext(a);
     }
     seg = b.seq_segs + h * rt + r;
-    cut(x, ext);
+    cut(x, e);
   }
-  __device__ __forceinline__ bool next(const AttendArgs& a, const Begin& b) {
+  __device__ __forceinline__ bool next(const AttendArgs& a) {
     if (left <= 0) return false;
-    int ext;
+    int e;
+#pragma unroll 1
     do {
       ++seg;
-      if (++r == rt) {
+      ++r;
+      if (rows_left() <= 0) {
         r = 0;
         if (++h == a.heads) {
           h = 0;
+#pragma unroll 1
           do {
             if (++seq >= a.n) {   // lengths that changed under way
               left = 0;
               return false;
             }
-            enter(a, b);
-          } while (rt == 0);
+            enter(a);
+          } while (rows == 0);
         }
       }
-      ext = tile(a, b);
-    } while (ext == 0);
-    cut(0, ext);
+      e = ext(a);
+    } while (e == 0);
+    cut(0, e);
     return true;
   }
 };
@@ -417,11 +433,10 @@ template <class T, int D>
 __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int S = kFewStages<D>, CH = D / 8;   // stages, 16-byte chunks of a row
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long plan_sm[12];
   __shared__ float2 stat[4][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const Begin b = plan_block<FewCut, kFewThreads>(a, plan_sm);
+  const Begin b = plan_block<FewCut, kFewThreads>(a);
   if (b.u0 >= b.u1) return;
   const uint32_t ring = shared_addr(smem) + warp * S * kFewStage<D>;
   float* joined = reinterpret_cast<float*>(smem + 4 * S * kFewStage<D>);
@@ -433,8 +448,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   bool more = true;
   int page[2] = {0, 0};
   auto fetch_pages = [&]() {
+#pragma unroll 1
     while (more && lt >= lp.t1) {
-      more = lp.next(a, b);
+      more = lp.next(a);
       lt = lp.t0;
     }
     if (!more) return;
@@ -469,7 +485,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < S - 1; ++s) issue(s);
 
   Piece<FewCut> w;
@@ -489,7 +505,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = w.r * kFewRows + g + 8 * i;
-      const int tok = row / a.group;
+      const int tok = a.by_group(row);
       const bool in = row < w.rows;
       lim[i] = in ? w.sees(tok) : 0;
       const unsigned char* src =
@@ -625,7 +641,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       }
       __syncthreads();
     }
-  } while (w.next(a, b));
+  } while (w.next(a));
   if (bad) atomicOr(a.status, bad);
 }
 
@@ -636,35 +652,46 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
 // tokens.
 //
 // A block has two softmax groups of four warps, each with a tile of 128 query
-// rows in shared memory, its scores (fp32, 128 columns; the weights take their
-// place as 16-bit pairs in the first 64) and its output (fp32) in tensor
-// memory: 2 x (128 + 128) columns, all 512.  One warp loads K and V tiles of
-// 128 keys by TMA, page by page, into a ring; one thread issues the products:
+// rows in shared memory.  One warp loads K and V tiles of 128 keys by TMA, page
+// by page, into rings; two warps issue the products of a group each:
 //   S = Q K^T (both from shared memory), O += P V (P from tensor memory, V as
 //   it lies, keys down, i.e. N-major).
 // Each thread of a group owns one row, so the row's maximum and sum need no
-// exchange.  While one group takes its softmax the other's products run: the
-// issue order is PV(v), QK(v + 2) for steps v = 0, 1, ..., step v belonging to
-// group v % 2, and since the tensor core works in that order, S(v + 2) being
-// complete means that PV(v) is: no other barrier guards a group's scores or
-// its output.
+// exchange.
 //   wide segments (more than 128 rows): the groups have different rows and
 //   share every K and V tile, which halves what has to come out of L2;
 //   others: the groups have the same rows and take every other key tile.
 // Each group leaves a partial of its own, so a slot has two `ways`.
+//
+// Tensor memory, of each group: S (fp32, 128 columns), whose first 64 columns
+// then hold P (16-bit pairs), and O (fp32, D columns): all 512 for D = 128.
+// A group is one chain, S(i) -> softmax -> PV(i) -> QK(i + 1), and while one is
+// in its softmax the other's products run; PV starts when half of P is there.
+// The tensor core takes a group's products in order, so S(i + 1) being complete
+// means that PV(i) is, and no barrier guards P or O.  (Tiles of 64 keys with P
+// beside S, whose QK(i + 1) runs beside softmax i, have a shorter chain but fetch
+// Q twice as often, 192 bytes of shared memory a cycle where there are 128:
+// 4000 cycles for 256 rows x 128 keys against KCYC here; arithmetic alone takes
+// 2048.)
 // The running maximum is raised, and O rescaled in tensor memory, only when a
 // tile's maximum exceeds it by more than 8 (a factor 256, which the 16-bit
 // weights and fp32 sums hold without loss of precision), i.e. hardly ever after
 // the first tiles.  V rows past the end of the keys are zeroed in shared memory
 // (0 x NaN is not 0), scores there are masked, so K may hold anything.
-constexpr int kTile = 128;         // rows of a group's query tile; keys of a K or V tile
-constexpr int kManyThreads = 384;   // two softmax groups, and one whose first two warps load and multiply
-// The launch's registers, 168 a thread, are shared out again: 2 x 216 + 72 = 3 x 168.
-constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
-template <int D> constexpr int kTileBytes = kTile * D * 2;
-template <int D> constexpr int kRing = D == 128 ? 5 : 10;   // K and V tiles in flight
-template <int D> constexpr int kManySmem = (2 + kRing<D>) * kTileBytes<D> + 1024;
+constexpr int kTile = 128;          // rows of a group's query tile
+constexpr int kKeys = ManyCut::kKeys;
+constexpr int kManyThreads = 384;   // two softmax groups, and one whose first three warps load and multiply
+// The launch's registers, 168 a thread, are shared out again: 2 x 208 + 88 = 3 x 168.
+constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;
+template <int D> constexpr int kQueryBytes = kTile * D * 2;
+template <int D> constexpr int kKeyBytes = kKeys * D * 2;
+// K and V tiles in flight (a K tile is done with half a step earlier).
+template <int D> constexpr int kRingK = D == 128 ? 2 : 4;
+template <int D> constexpr int kRingV = D == 128 ? 3 : 6;
+template <int D> constexpr int kManySmem = 2 * kQueryBytes<D> + (kRingK<D> + kRingV<D>) * kKeyBytes<D> + 1024;
 constexpr float kRaise = 8.f;
+constexpr int kPolyOf8 = 3;   // of eight pairs of weights, how many exp2_poly takes: the special-function unit's share is
+                              // then below the products' time
 
 __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(b)), "r"(n) : "memory");
@@ -684,6 +711,17 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Have both phases ended?
+__device__ __forceinline__ bool mbar_try2(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %5;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4, %5;\n\tand.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(shared_addr(x)), "r"(px), "r"(shared_addr(y)), "r"(py), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
 // Bounded: false when the phase has not completed after kSpinLimit polls.
 __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity) {
   for (int i = 0; i < lb::kSpinLimit; ++i)
@@ -695,6 +733,11 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(shared_addr(bar))
                : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // Matrix descriptor, 128-byte swizzle: lead = bytes between blocks of 64
 // N-values (N-major only), step = bytes between groups of eight 128-byte rows.
@@ -732,6 +775,20 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t* r) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
+}
+__device__ __forceinline__ void tmem_load8(uint32_t at, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // The registers of a load are good after this: passing them through keeps every use behind the wait.
 __device__ __forceinline__ void tmem_load_wait(uint32_t* r) {
@@ -776,10 +833,27 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// The largest of three, NaN if one is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+// 2^x of two values of at most 2^7 on the multiply-add units: x = n + r with n the nearest whole number (the sum with
+// 1.5 * 2^23 rounds to it), 2^r by the polynomial of degree 4 with the smallest largest relative error on [-1/2, 1/2]
+// (2.6e-6, by Remez exchange), and n added to the exponent.  Below -126: about 2^-126.
+__device__ __forceinline__ float2 exp2_poly(uint64_t x) {
+  float2 v = split(x);
+  const uint64_t c = pair(fmaxf(v.x, -126.f), fmaxf(v.y, -126.f));
+  const uint64_t t = add2(c, pair(12582912.f, 12582912.f));
+  const uint64_t r = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), c);
+  uint64_t p = fma2(r, pair(0.009570102207362652f, 0.009570102207362652f), pair(0.05591785907745361f, 0.05591785907745361f));
+  p = fma2(p, r, pair(0.240247443318367f, 0.240247443318367f));
+  p = fma2(p, r, pair(0.6931217908859253f, 0.6931217908859253f));
+  p = fma2(p, r, pair(0.9999992847442627f, 0.9999992847442627f));
+  const float2 q = split(p), n = split(t);
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
+                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -796,17 +870,26 @@ template <class T, int D>
 __global__ void __launch_bounds__(kManyThreads, 1)
     many_rows_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v) {
-  constexpr int R = kRing<D>, TB = kTileBytes<D>, HALF = kTile * 128;   // HALF: bytes of 64 columns of a tile
+  constexpr int RK = kRingK<D>, RV = kRingV<D>, QB = kQueryBytes<D>, KB = kKeyBytes<D>;
+  constexpr int QHALF = kTile * 128, KHALF = kKeys * 128;   // bytes of 64 columns of a tile
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (shared_addr(smem_raw) & 1023)) & 1023);
   unsigned char* const qs = smem;            // [2] query tiles
-  unsigned char* const ring = smem + 2 * TB;
-  __shared__ __align__(8) uint64_t full[R], empty[R], s_full[2], p_full[2], o_full[2], q_full[2];
+  unsigned char* const ks = smem + 2 * QB;   // [RK] K tiles
+  unsigned char* const vs = ks + RK * KB;    // [RV] V tiles
+  // k_full, v_full: a ring slot holds its tile; k_free: it has been read (both groups say so, or one twice), v_free:
+  // likewise; q_full: a group's queries are in place; s_full: its scores are complete; p_full: the first, second half
+  // of its weights are in place; o_full: a piece's last PV is done.
+  // A parity tells whether a phase has ended only to one who knows that the phase before it has.  Within a group that
+  // follows from the order of its steps.  A ring slot's last tile may have been the other group's: `loads` counts the
+  // tiles whose loads have begun, and one begins only when the slot's last tile has landed and been read.
+  __shared__ __align__(8) uint64_t k_full[RK], k_free[RK], v_full[RV], v_free[RV];
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[4], o_full[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ long long plan_sm[28];
+  __shared__ volatile uint32_t loads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const Begin b = plan_block<ManyCut, kManyThreads>(a, plan_sm);
+  const Begin b = plan_block<ManyCut, kManyThreads>(a);
   if (b.u0 >= b.u1) return;   // the whole block
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(shared_addr(&tmem_slot))
@@ -814,15 +897,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < R; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    loads = 0;
+    for (int i = 0; i < RK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_free[i], 2);
+    }
+    for (int i = 0; i < RV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_free[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&o_full[i], 1);
       mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&o_full[i], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -832,8 +921,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const uint32_t tmem = tmem_slot;
   bool dead = false;   // a wait ran out: go on without waiting, report, end
   unsigned bad = 0;
-  // K tile number 2 n and V tile 2 n + 1 of the n-th key tile; tile x is in slot x % R
-  uint32_t n = 0;
+  uint32_t n = 0;      // key tiles of the pieces before: the block's x-th is in slots x % RK and x % RV
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
@@ -841,12 +929,23 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     pc.begin(a, b);
     if (warp == 8) {
       // ---- loads: lane i brings the i-th page of a tile
-      const int box = min(1 << a.page_shift, kTile);   // rows of a copy
-      uint32_t issued = 0;
+      const int box = min(1 << a.page_shift, kKeys);   // rows of a copy
+      auto load = [&](const CUtensorMap* map, unsigned char* slot, uint64_t* full, int key, int boxes, int page) {
+        if (lane == 0) mbar_expect(full, boxes * box * D * 2);
+        __syncwarp();
+        if (lane < boxes) {
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_page(slot + h * KHALF + lane * box * 128, map, 64 * h, key & ((1 << a.page_shift) - 1), pc.h, page, full);
+        }
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar, parity));
+      };
       do {
         for (int t = pc.t0; t < pc.t1; ++t, ++n) {
-          const int key = t * kTile + lane * box;
-          const int held = min(kTile, pc.len - t * kTile);
+          const int key = t * kKeys + lane * box;
+          const int held = min(kKeys, pc.len - t * kKeys);
           const int boxes = (held + box - 1) / box;
           int page = 0;
           if (lane < boxes) {
@@ -856,77 +955,86 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               bad |= kStatusIndex;
             }
           }
-  #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t x = 2 * n + kv;
-            const int slot = x % R;
-            if (x >= R && !dead && !mbar_wait(&empty[slot], (x / R - 1) & 1)) dead = true;
-            dead = __any_sync(0xffffffffu, dead);
-            if (dead) break;
-            if (lane == 0) mbar_expect(&full[slot], boxes * box * D * 2);
-            __syncwarp();
-            issued = x + 1;
-            if (lane < boxes) {
-  #pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                tma_page(ring + slot * TB + h * HALF + lane * box * 128, kv ? &map_v : &map_k, 64 * h,
-                         key & ((1 << a.page_shift) - 1), pc.h, page, &full[slot]);
-            }
-          }
+          if (n >= RK) wait(&k_free[n % RK], (n / RK - 1) & 1);
+          if (n >= RV) wait(&v_free[n % RV], (n / RV - 1) & 1);
           if (dead) break;
-        }
-      } while (!dead && pc.next(a, b));
-      if (dead && lane == 0)   // copies under way land before the block ends
-        for (uint32_t x = issued > R ? issued - R : 0; x < issued; ++x) mbar_wait(&full[x % R], (x / R) & 1);
-    } else if (warp == 9) {
-      // ---- products
-      if (lane == 0) {
-        constexpr uint32_t pv = mma_shape<T>(kTile, D, true);
-        // a negative scale negates the queries, so that the softmax knows positive ones only
-        const uint32_t qk = mma_shape<T>(kTile, kTile, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
-        uint32_t steps[2] = {0, 0}, pieces[2] = {0, 0};
-        do {
-          const bool wide = pc.rows_left() > kTile;
-          const int tiles = pc.t1 - pc.t0, nv = wide ? 2 * tiles : tiles;
-          auto score = [&](int v) {   // S of step v
-            const int g = v & 1;
-            const uint32_t x = 2 * (n + (wide ? v >> 1 : v));
-            if (v < 2) {
-              if (!dead && !mbar_wait(&q_full[g], pieces[g] & 1)) dead = true;
-              ++pieces[g];
-            }
-            if (!dead && !mbar_wait(&full[x % R], (x / R) & 1)) dead = true;
-            tc_after();
-            const uint32_t q = shared_addr(qs + g * TB), k = shared_addr(ring + x % R * TB);
-  #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-              const uint32_t off = (s >> 2) * HALF + (s & 3) * 32;
-              mma_ss(tmem + 128 * g, tile_desc(q + off, 16, 1024), tile_desc(k + off, 16, 1024), qk, s > 0);
-            }
-            tc_commit(&s_full[g]);
-            if (!wide || g == 1) tc_commit(&empty[x % R]);
-          };
-          if (nv > 0) score(0);
-          if (nv > 1) score(1);
-          for (int v = 0; v < nv; ++v) {
-            const int g = v & 1;
-            const uint32_t x = 2 * (n + (wide ? v >> 1 : v)) + 1;
-            if (!dead && !mbar_wait(&p_full[g], steps[g] & 1)) dead = true;
-            ++steps[g];
-            if (!dead && !mbar_wait(&full[x % R], (x / R) & 1)) dead = true;
-            tc_after();
-            const uint32_t vt = shared_addr(ring + x % R * TB);
-  #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-              mma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 8 * s, tile_desc(vt + s * 2048, HALF, 1024), pv,
-                     v >= 2 || s > 0);
-            if (!wide || g == 1) tc_commit(&empty[x % R]);
-            if (v + 2 < nv) score(v + 2);
-            else tc_commit(&o_full[g]);
+          load(&map_k, ks + n % RK * KB, &k_full[n % RK], key, boxes, page);
+          load(&map_v, vs + n % RV * KB, &v_full[n % RV], key, boxes, page);
+          if (lane == 0) {
+            __threadfence_block();
+            loads = n + 1;
           }
-          n += tiles;
-        } while (!dead && pc.next(a, b));
+        }
+      } while (!dead && pc.next(a));
+      if (dead && lane == 0) {   // copies under way land before the block ends
+        for (uint32_t x = n > RK ? n - RK : 0; x < n; ++x) mbar_wait(&k_full[x % RK], (x / RK) & 1);
+        for (uint32_t x = n > RV ? n - RV : 0; x < n; ++x) mbar_wait(&v_full[x % RV], (x / RV) & 1);
       }
+    } else if (warp < 11) {
+      // ---- products of group g.  The whole warp walks, one elected lane issues: control flow and operands that are
+      // uniform for the warp let descriptors live in uniform registers (with lane 0 alone in a branch, moving them
+      // there took 65 cycles a product, more than the tensor core needs for it).  One warp for both groups was not
+      // enough: a product's waits, issue and commit take it some 500 cycles.
+      const int g = warp - 9;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + 128 * g;   // S, P, P; O 256 columns on
+      constexpr uint32_t pv = mma_shape<T>(kTile, D, true);
+      // a negative scale negates the queries, so that the softmax knows positive ones only
+      const uint32_t qk = mma_shape<T>(kTile, kKeys, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+      const uint64_t q = tile_desc(shared_addr(qs) + g * QB, 16, 1024);
+      uint32_t s = 0, pieces = 0;       // steps, pieces with steps before
+      uint32_t begun = 0;               // loads, as last seen
+      // both barriers at once: their latencies are most of what a step costs this warp
+      auto wait = [&](uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) {
+        for (int spin = 0; !dead && !mbar_try2(x, px, y, py); ++spin) dead = spin > lb::kSpinLimit;
+      };
+      do {
+        const bool wide = __shfl_sync(0xffffffffu, (int)(pc.rows_left() > kTile), 0);
+        const int tiles = __shfl_sync(0xffffffffu, pc.t1 - pc.t0, 0);
+        const int total = wide ? tiles : (tiles - g + 1) / 2;
+        const uint32_t inc = wide ? 1 : 2;
+        uint32_t x = n + (wide ? 0 : g);   // the step's tile
+        uint32_t vslot = x % RV, vphase = (x / RV) & 1;
+        for (int i = 0; i < total; ++i, ++s, x += inc) {
+          for (int spin = 0; begun <= x && !dead; ++spin) {
+            begun = __shfl_sync(0xffffffffu, loads, 0);
+            dead = spin > lb::kSpinLimit;
+          }
+          wait(&k_full[x % RK], (x / RK) & 1, &q_full[g], pieces & 1);
+          tc_after();
+          const uint64_t k = tile_desc(shared_addr(ks) + x % RK * KB, 16, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+              mma_ss(tm, q + ((c >> 2) * QHALF + (c & 3) * 32) / 16, k + ((c >> 2) * KHALF + (c & 3) * 32) / 16, qk, c > 0);
+            tc_commit(&s_full[g]);
+          }
+          __syncwarp();
+          const uint64_t v = tile_desc(shared_addr(vs) + vslot * KB, KHALF, 1024);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            wait(&v_full[vslot], vphase, &p_full[2 * g + half], s & 1);
+            tc_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int c = 4 * half; c < 4 * half + 4; ++c)
+                mma_ts(tm + 256, tm + 8 * c, v + c * 2048 / 16, pv, i > 0 || c > 0);
+              if (half) {
+                tc_commit(&v_free[vslot]);
+                if (!wide) mbar_arrive(&v_free[vslot]);
+                if (i + 1 == total) tc_commit(&o_full[g]);
+              }
+            }
+            __syncwarp();
+          }
+          vslot += inc;
+          if (vslot >= RV) {
+            vslot -= RV;
+            vphase ^= 1;
+          }
+        }
+        pieces += total > 0;
+        n += tiles;
+      } while (!dead && pc.next(a));
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -948,15 +1056,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // The group's queries for a piece, under way: the products that read the last ones are done by then.
     auto load_queries = [&](const Piece<ManyCut>& x) {
       if (steps_of(x) > 0) {
-        const int at = row_of(x), tok = at / a.group;
+        const int at = row_of(x), tok = a.by_group(at);
         const bool in = at < x.rows;
         const unsigned char* src =
             in ? a.q + (long long)(x.first + tok) * a.q_token + (long long)(x.h * a.group + at - tok * a.group) * a.q_head
                : a.q;
-        const uint32_t dst = shared_addr(qs + g * TB) + row * 128;
+        const uint32_t dst = shared_addr(qs + g * QB) + row * 128;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
-          copy16(dst + (c >> 3) * HALF + (((c & 7) ^ (row & 7)) << 4), src + (in ? 16 * c : 0), in ? 16 : 0);
+          copy16(dst + (c >> 3) * QHALF + (((c & 7) ^ (row & 7)) << 4), src + (in ? 16 * c : 0), in ? 16 : 0);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -966,7 +1074,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int tiles = pc.t1 - pc.t0, mine = steps_of(pc);
       const bool wide = pc.rows_left() > kTile;
       const int at = row_of(pc);
-      const int lim = at < pc.rows ? pc.sees(at / a.group) : 0;
+      const int lim = at < pc.rows ? pc.sees(a.by_group(at)) : 0;
       float m = -INFINITY, l = 0.f;
       if (mine > 0) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -975,84 +1083,102 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (lane == 0) mbar_arrive(&q_full[g]);
         for (int j = 0; j < mine; ++j, ++steps) {
           const int tile = wide ? j : 2 * j + g;
-          const int key = (pc.t0 + tile) * kTile;
+          const int key = (pc.t0 + tile) * kKeys;
           if (!dead && !mbar_wait(&s_full[g], steps & 1)) dead = true;
           dead = __any_sync(0xffffffffu, dead);
           tc_after();
-          uint32_t s[kTile];
+          if ((threadIdx.x & 127) == 0) {   // the products that made these scores have read the K tile
+            mbar_arrive(&k_free[(n + tile) % RK]);
+            if (!wide) mbar_arrive(&k_free[(n + tile) % RK]);
+          }
+          uint32_t s[kKeys];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_load32(ts + 32 * c, s + 32 * c);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_load_wait(s + 32 * c);
-          if (__any_sync(0xffffffffu, key + kTile > lim)) {
+          if (__any_sync(0xffffffffu, key + kKeys > lim)) {
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
+            for (int i = 0; i < kKeys; ++i)
               if (key + i >= lim) s[i] = 0xff800000u;   // -inf
           }
           // four chains each, so that their latency is covered with two warps a scheduler
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kTile; i += 8)
+          for (int i = 0; i < kKeys; i += 8)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               tops[c] = max3(tops[c], __uint_as_float(s[i + 2 * c]), __uint_as_float(s[i + 2 * c + 1]));
-          const float top = scale * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-          const bool raise = top > m + kRaise;
+          const float top = scale * max3(max3(tops[0], tops[1], tops[2]), tops[3], -INFINITY);
+          const bool raise = !(top <= m + kRaise);   // also if a score is NaN
           if (__any_sync(0xffffffffu, raise)) {
-            const float f = raise ? exp2_fast(m - top) : 1.f;
-            if (raise) m = top;
+            const float to_m = top < INFINITY ? top : NAN;   // inf - inf is none either
+            const float f = raise ? exp2_fast(m - to_m) : 1.f;
+            if (raise) m = to_m;
             l *= f;
-            if (j > 0) {
+            if (j > 0) {   // rare: small steps, as the scores fill the registers
+#pragma unroll 1
+              for (int c = 0; c < D; c += 8) {
+                uint32_t o[8];
+                tmem_load8(to + c, o);
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_load32(to + 32 * c, o);
-                tmem_load_wait(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_store32(to + 32 * c, o);
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_store8(to + c, o);
               }
             }
           }
-          const float base = m == -INFINITY ? 0.f : m;
-          const uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
-          uint64_t sums[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int i = 0; i < kTile / 2; ++i) {
-            const float2 x = split(fma2(pair(s[2 * i], s[2 * i + 1]), scale2, base2));
-            const float p = exp2_fast(x.x), q = exp2_fast(x.y);
-            sums[i & 3] = add2(sums[i & 3], pair(p, q));
-            s[i] = Mma<T>::pack(p, q);
-          }
-          const float2 sum = split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
-          l += sum.x + sum.y;
-          tmem_store32(ts, s);
-          tmem_store32(ts + 32, s + 32);
-          tmem_store_wait();
-          if (pc.len - key < kTile && (!wide || g == 0)) {   // V rows past the end
-            const uint32_t x = 2 * (n + tile) + 1;
-            if (!dead && !mbar_wait(&full[x % R], (x / R) & 1)) dead = true;
+          if (pc.len - key < kKeys) {   // V rows past the end (both groups of a wide segment write the same zeros)
+            const uint32_t x = n + tile;
+            if (!dead && !mbar_wait(&v_full[x % RV], (x / RV) & 1)) dead = true;
             if (row >= pc.len - key) {
 #pragma unroll
               for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(ring + x % R * TB + (c >> 3) * HALF + row * 128 + (c & 7) * 16) =
+                *reinterpret_cast<uint4*>(vs + x % RV * KB + (c >> 3) * KHALF + row * 128 + (c & 7) * 16) =
                     make_uint4(0, 0, 0, 0);
             }
             async_fence();
             dead = __any_sync(0xffffffffu, dead);
           }
-          tc_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[g]);
+          const float base = m == -INFINITY ? 0.f : m;
+          const uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
+          uint64_t sums[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i0 = 32 * half; i0 < 32 * half + 32; i0 += 8) {
+              // eight pairs at a time, and no more in flight: the scores fill the registers
+              asm volatile("" ::: "memory");
+              uint64_t x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = fma2(pair(s[2 * (i0 + i)], s[2 * (i0 + i) + 1]), scale2, base2);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float2 e;
+                if (i < kPolyOf8) {
+                  e = exp2_poly(x[i]);
+                } else {
+                  e = split(x[i]);
+                  e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                }
+                sums[i & 3] = add2(sums[i & 3], pair(e.x, e.y));
+                s[i0 + i] = Mma<T>::pack(e.x, e.y);
+              }
+            }
+            tmem_store32(ts + 32 * half, s + 32 * half);
+            tmem_store_wait();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * g + half]);
+          }
+          const float2 sum = split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+          l += sum.x + sum.y;
         }
       }
       Piece<ManyCut> nx = pc;
-      more = nx.next(a, b);
+      more = nx.next(a);
       if (more) load_queries(nx);
       if (mine > 0) {
-        if (!dead && !mbar_wait(&o_full[g], pieces & 1)) dead = true;
+        if (!dead && !mbar_wait(&o_full[g], pieces++ & 1)) dead = true;
         dead = __any_sync(0xffffffffu, dead);
-        ++pieces;
         tc_after();
       }
       // ---- the partial: rows of one way, or two ways of the same rows
@@ -1098,14 +1224,14 @@ struct Source {
   const float2* ml;
   const float* part;
   int few;                    // of few_rows_kernel, else of many_rows_kernel
-  int ways;                   // partials of a slot
   int rows_alloc, n_partials;
 };
 struct JoinArgs {
-  Source prefix, own;   // prefix.head null: no prefix
+  Source set[2];   // the own keys', the prefix's (head null: no prefix)
   unsigned char* out;
   long long out_token, out_head;   // bytes
   int n, n_tokens, heads, group;
+  Divisor by_group;
 };
 
 // One warp per (token, query head): finds the token's sequence, weighs the
@@ -1120,77 +1246,89 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   if (threadIdx.x == 0) s_seq = -1;
   __syncthreads();
   for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
-    const int first = a.own.seqs[i].first, count = a.own.seqs[i].count;
+    const int first = a.set[0].seqs[i].first, count = a.set[0].seqs[i].count;
     if (t >= first && t < first + count) s_seq = i;
   }
   __syncthreads();
   const int seq = s_seq;
   if (seq < 0 || h >= a.heads * a.group) return;
-  const int kv = h / a.group, sub = h - kv * a.group;
+  const int kv = a.by_group(h), sub = h - kv * a.group;
   float acc[E] = {}, m = -INFINITY, l = 0.f;
-
-  // the partials of one segment (units ua .. ua + ext - 1), ways w0 .. w1 - 1 of each slot, row `row` of them
-  auto add = [&](const Source& S, int seg, long long ua, int ext, int w0, int w1, int row) {
-    if (ext <= 0) return;
-    const long long W = S.head->width, ub = ua + ext - 1;
-    int c0, c1;
-    if ((ub | W) >> 32 == 0) {   // nearly always: two divisions of 32 bits
-      c0 = (int)((uint32_t)ua / (uint32_t)W);
-      c1 = (int)((uint32_t)ub / (uint32_t)W);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const Source& S = a.set[which];
+    if (!S.head) continue;
+    const PlanHead H = *S.head;
+    if (H.width == 0) return;
+    // the row's segment: units ua .. ua + ext - 1
+    const int tile = S.few ? FewCut::kRows : ManyCut::kRows;
+    auto extent_of = [&](int tiles, int left) {
+      return S.few ? extent<FewCut>(tiles, left) : extent<ManyCut>(tiles, left);
+    };
+    int row, left, r, ua, ext, seg;
+    if (which) {
+      row = (t - H.t0) * a.group + sub;
+      r = row / (unsigned)tile;
+      left = H.p_rows - r * tile;
+      ua = kv * H.p_head + r * extent_of(H.p_kt, tile);
+      ext = extent_of(H.p_kt, left);
+      seg = kv * H.p_rt + r;
     } else {
-      c0 = (int)(ua / W);
-      c1 = (int)(ub / W);
-    }
-    for (int c = c0; c <= c1; ++c)
-      for (int way = w0; way < w1; ++way) {
-        const long long x = (seg + (long long)c) * S.ways + way, at = x * S.rows_alloc + row;
-        if (x >= S.n_partials) continue;
-        const float2 p = S.ml[at];
-        if (p.x == -INFINITY) continue;   // nothing seen; its output row need not have been written
-        float v[E];
-        if constexpr (E == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(S.part + at * D + lane * 4);
-          v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(S.part + at * D + lane * 2);
-          v[0] = y.x, v[1] = y.y;
-        }
-        const float now = fmaxf(m, p.x);
-        const float f0 = exp2_fast(m - now), f1 = exp2_fast(p.x - now);
-        m = now;
-        l = l * f0 + p.y * f1;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
+      const SeqPlan s = S.seqs[seq];
+      const int rows = s.count * a.group;
+      row = (t - s.first) * a.group + sub;
+      r = row / (unsigned)tile;
+      left = rows - r * tile;
+      auto own = [&](int i) {
+        return extent_of(S.few ? own_tiles<FewCut>(a.by_group, rows, s.len, s.before, i)
+                               : own_tiles<ManyCut>(a.by_group, rows, s.len, s.before, i), rows - i * tile);
+      };
+      int before = 0;   // units of the head's row tiles before this one
+      if (r > 0) {
+#pragma unroll 1
+        for (int i = lane; i < r; i += 32) before += own(i);
+        before = __reduce_add_sync(0xffffffffu, before);
       }
-  };
-  auto prefix_set = [&](auto cut) {
-    using C = decltype(cut);
-    const PlanHead H = *a.prefix.head;
-    const int row = (t - H.t0) * a.group + sub, r = row / C::kRows, in = row - r * C::kRows;
-    const int left = H.p_rows - r * C::kRows;
-    const bool wide = C::cost(left) > 1;
-    add(a.prefix, kv * H.p_rt + r, (long long)kv * H.p_head + (long long)r * extent<C>(H.p_kt, C::kRows),
-        extent<C>(H.p_kt, left), wide ? in >> 7 : 0, wide ? (in >> 7) + 1 : a.prefix.ways, wide ? in & 127 : in);
-  };
-  auto own_set = [&](auto cut) {
-    using C = decltype(cut);
-    const SeqPlan s = a.own.seqs[seq];
-    const int row = (t - s.first) * a.group + sub, r = row / C::kRows, in = row - r * C::kRows;
-    const int left = s.count * a.group - r * C::kRows;
-    const bool wide = C::cost(left) > 1;
-    int before = 0;   // units of the head's row tiles before this one
-    for (int i = lane; i < r; i += 32) before += own_extent<C>(s.count, a.group, s.len, s.before, i);
-    before = __reduce_add_sync(0xffffffffu, before);
-    add(a.own, s.segs_before + kv * row_tiles<C>(s.count * a.group) + r,
-        s.units_before + (long long)kv * s.head + before, own_extent<C>(s.count, a.group, s.len, s.before, r),
-        wide ? in >> 7 : 0, wide ? (in >> 7) + 1 : a.own.ways, wide ? in & 127 : in);
-  };
-  if (a.prefix.head) {
-    if (a.prefix.few) prefix_set(FewCut{});
-    else prefix_set(ManyCut{});
+      ua = s.units_before + kv * s.head + before;
+      ext = own(r);
+      seg = s.segs_before + kv * ((rows + tile - 1) / (unsigned)tile) + r;
+    }
+    if (ext == 0) continue;
+    // its partials: few rows one a block; many rows the way of the row's half of a wide tile, or two
+    row -= r * tile;
+    const int c0 = (unsigned)ua / (unsigned)H.width, c1 = (unsigned)(ua + ext - 1) / (unsigned)H.width;
+    int x = seg + c0, end = seg + c1 + 1, step = 1;
+    if (!S.few) {
+      x *= 2;
+      end *= 2;
+      if (left > 128) {
+        x += row >> 7;
+        row &= 127;
+        step = 2;
+      }
+    }
+    end = min(end, S.n_partials);
+#pragma unroll 2
+    for (; x < end; x += step) {
+      const long long at = (long long)x * S.rows_alloc + row;
+      const float2 p = S.ml[at];
+      if (p.x == -INFINITY) continue;   // nothing seen; its output row need not have been written
+      float v[E];
+      if constexpr (E == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(S.part + at * D + lane * 4);
+        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(S.part + at * D + lane * 2);
+        v[0] = y.x, v[1] = y.y;
+      }
+      const float now = fmaxf(m, p.x);
+      const float f0 = exp2_fast(m - now), f1 = exp2_fast(p.x - now);
+      m = now;
+      l = l * f0 + p.y * f1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
+    }
   }
-  if (a.own.few) own_set(FewCut{});
-  else own_set(ManyCut{});
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
   T r[E];
 #pragma unroll
@@ -1211,6 +1349,13 @@ int sm_count() {
     return cudaDeviceGetAttribute(&out, cudaDevAttrMultiProcessorCount, dev);
   });
   return e || v < 1 ? 148 : v;
+}
+
+Divisor divisor(int d) {
+  Divisor r{0, 0};
+  while ((1u << r.shift) < (unsigned)d) ++r.shift;
+  r.mul = (unsigned)((((uint64_t)1 << 32) * (((uint64_t)1 << r.shift) - d)) / d + 1);
+  return r;
 }
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
@@ -1298,7 +1443,7 @@ lb_status plane_map(const lb_cache& c, const lb_plane& P, CUtensorMap* map) {
   const cuuint64_t dim[4] = {(cuuint64_t)P.width, (cuuint64_t)c.page_size, (cuuint64_t)P.heads, (cuuint64_t)c.n_pages};
   const cuuint64_t st[3] = {stride(P.stride_row, c.page_size), stride(P.stride_head, P.heads),
                             stride(P.stride_page, c.n_pages)};
-  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(c.page_size, kTile), 1, 1}, one[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(c.page_size, kKeys), 1, 1}, one[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, P.dt == LB_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                         P.data, dim, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1335,7 +1480,9 @@ lb_status check_attend(const lb_cache* c, int k, int heads_q, int n_tokens, int 
   if (K.dt != LB_F16 && K.dt != LB_BF16) return LB_ERR_UNSUPPORTED;
   if (K.width != 64 && K.width != 128) return LB_ERR_UNSUPPORTED;
   if (K.heads < 1 || heads_q < 1 || heads_q % K.heads || heads_q > 4096) return LB_ERR_SHAPE;
-  if (n < 1 || n > 4096 || n_tokens < 0 || n_tokens > 1 << 20 || most_q < 1) return LB_ERR_SHAPE;
+  if (n < 1 || n > 4096 || n_tokens < 0 || most_q < 1) return LB_ERR_SHAPE;
+  // units, rows and keys are counted in 31 bits
+  if ((int64_t)n_tokens * heads_q > 1 << 22 || (int64_t)c->max_pages * c->page_size > 1 << 24) return LB_ERR_SHAPE;
   return LB_OK;
 }
 
@@ -1400,6 +1547,7 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   a.most_q = most_q;
   a.heads = K.heads;
   a.group = group;
+  a.by_group = divisor(group);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = status;
   JoinArgs j{};
@@ -1413,9 +1561,9 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
     x.part = reinterpret_cast<float*>(w + g.part);
     x.rows_alloc = g.rows_alloc;
     x.n_partials = (int)g.partials;
-    const Source src{x.head, x.seqs, x.ml, x.part, g.ways == 1, g.ways, g.rows_alloc, (int)g.partials};
-    if (own) j.own = src;
-    if (with_prefix) j.prefix = src;
+    const Source src{x.head, x.seqs, x.ml, x.part, g.ways == 1, g.rows_alloc, (int)g.partials};
+    if (own) j.set[0] = src;
+    if (with_prefix) j.set[1] = src;
     return x;
   };
   unsigned char* w = static_cast<unsigned char*>(work);
@@ -1428,6 +1576,7 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   j.n_tokens = n_tokens;
   j.heads = K.heads;
   j.group = group;
+  j.by_group = a.by_group;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (K.dt == LB_F16)
     e = D == 128 ? launch<__half, 128>(s, few, many, map_k, map_v, j, st)
