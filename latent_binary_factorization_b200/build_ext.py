@@ -1,4 +1,5 @@
-"""Build liblittlebit.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Build liblittlebit.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_cache.so, the compiled marshalling of cache.py, beside it with g++."""
 from __future__ import annotations
 
 import os
@@ -10,6 +11,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "liblittlebit.so")
+BINDING = os.path.join(HERE, "_cache.so")
 SOURCES = ["littlebit_capi.cu", "pack.cu", "decode.cu", "prefill.cu", "init.cu", "noalloc.cu", "selfcheck.cu", "cache.cu",
            "attend.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -44,5 +46,34 @@ def build(verbose: bool = False, force: bool = False) -> str:
     return LIB
 
 
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    """_cache.so, linked against torch and liblittlebit.so (build() it first)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    src = os.path.join(CSRC, "cache_binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "littlebit.h")]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(d) for d in deps):
+        return BINDING
+    includes = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(device_type="cuda")]
+    libs = cpp_extension.library_paths(device_type="cuda")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in includes], src,
+           "-o", BINDING, f"-L{HERE}", "-llittlebit", "-Wl,-rpath,$ORIGIN", *[f"-L{d}" for d in libs], "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd))
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or res.returncode != 0:
+        sys.stdout.write(res.stdout)
+        sys.stderr.write(res.stderr)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed with code {res.returncode}")
+    return BINDING
+
+
 if __name__ == "__main__":
     build(verbose="-v" in sys.argv, force=True)
+    build_binding(verbose="-v" in sys.argv, force=True)

@@ -2,122 +2,49 @@
 rows of tokens in pages, page bookkeeping, and attention over the pages of a
 batch that shares a prefix.
 
-Argument marshalling only, as in ``littlebit``: tensors are torch CUDA tensors,
-every step runs in the CUDA library, and nothing here waits for the GPU.  All
-calls take ``stream`` (a torch.cuda.Stream, default the current one of the
+Tensors are torch CUDA tensors, every step runs in the CUDA library, and
+nothing here waits for the GPU.  The marshalling of the arguments is compiled
+(csrc/cache_binding.cpp, ``_cache.so``): a call takes a few microseconds, as
+the kernels of a decode step do.  Arguments that do not fit raise ValueError,
+what the library refuses ``littlebit.LittleBitError``.
+
+All calls take ``stream`` (a torch.cuda.Stream, default the current one of the
 tensors' device); tensors that a call makes belong to that stream.  What the
 bookkeeping cannot do (no free page, an index outside the cache) is left out
 and reported by ``littlebit.device_status()``, bits 1 << 8 and 1 << 9.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import math
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
 from . import littlebit as lb
 
-_lib = lb.library()
-_P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_cache.so")
+if not os.path.exists(BINDING_PATH):
+    raise ImportError(
+        f"{BINDING_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'` "
+        "(the paged cache has no CPU implementation)"
+    )
+_loader = importlib.machinery.ExtensionFileLoader("_cache", BINDING_PATH)
+_b = importlib.util.module_from_spec(importlib.util.spec_from_loader("_cache", _loader))
+_loader.exec_module(_b)
+_b.on_fail(lb._check)
+
+_phases = lb.library().littlebit_rotary_phases
+_phases.restype = ctypes.c_int
+_phases.argtypes = [ctypes.c_int] + [ctypes.c_double] * 5 + [ctypes.c_int, ctypes.c_void_p]
 
 
-class LbPlane(ctypes.Structure):
-    _fields_ = [("data", _P), ("stride_page", _L), ("stride_head", _L), ("stride_row", _L), ("heads", _I),
-                ("width", _I), ("dt", _I)]
-
-
-class LbCache(ctypes.Structure):
-    _fields_ = [("planes", ctypes.POINTER(LbPlane)), ("n_planes", _I), ("n_pages", _I), ("page_size", _I),
-                ("n_slots", _I), ("max_pages", _I), ("table_stride", _L), ("table", _P), ("length", _P),
-                ("refs", _P)]
-
-
-class LbRows(ctypes.Structure):
-    _fields_ = [("data", _P), ("stride_token", _L), ("stride_head", _L), ("heads", _I), ("width", _I)]
-
-
-class LbRotary(ctypes.Structure):
-    _fields_ = [("phases", _P), ("rotary_dim", _I), ("interleaved", _I), ("scale", ctypes.c_float)]
-
-
-for _name, _args in {
-    "rotary_phases": [_I] + [ctypes.c_double] * 5 + [_I, _P],
-    "rotary": [_P, _P, _I, _I, _I, _P, _P, _I, _P],
-    "cache_extend": [_P, _P, _P, _I, _I, _I, _P, _P, _P],
-    "cache_locate": [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P],
-    "cache_write": [_P, _P, _P, _I, _I, _P, _P, _P, ctypes.c_uint, _P, _P, _P],
-    "cache_read": [_P, _P, _P, _I, _I, _P, _P],
-    "cache_fork": [_P, _P, _P, _I, _P, _P],
-    "cache_free": [_P, _P, _I, _P],
-    "cache_compact": [_P, _P, _P, _P, _P, _P],
-    "cache_copy": [_P, _P, _P, _I, _P],
-    "cache_attend": [_P, _I, _I, _P, _I, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
-}.items():
-    getattr(_lib, "littlebit_" + _name).restype = _I
-    getattr(_lib, "littlebit_" + _name).argtypes = _args
-for _name, _args in {"cache_fork_work": [_I], "cache_compact_work": [_I],
-                     "cache_attend_work": [_P, _I, _I, _I, _I, _I, _I]}.items():
-    getattr(_lib, "littlebit_" + _name).restype = ctypes.c_size_t
-    getattr(_lib, "littlebit_" + _name).argtypes = _args
-
-
-def _call(name: str, device: torch.device, stream, *args) -> None:
-    """The library call on ``stream``, with ``device`` current as it has to be."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+def _on(stream, device: torch.device):
+    """``stream`` as the current one of ``device`` (the binding takes the current)."""
+    if stream.device != device:
         raise ValueError(f"the stream is of {stream.device}, the tensors of {device}")
-    fn = getattr(_lib, name)
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            code = fn(*args, stream.cuda_stream)
-    if code:
-        raise lb.LittleBitError(code, name)
-
-
-def _making(stream):
-    """Tensors made inside belong to ``stream``."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _tensor(t, device, name: str) -> None:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
-
-
-def _list(t, device, name: str, n: int | None = None, dtype=torch.int32) -> int:
-    """A contiguous index tensor; its address."""
-    _tensor(t, device, name)
-    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {'n' if n is None else n} entries, got "
-                         f"{t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _rows(t, device, name: str, tokens: int | None = None, dtype=None) -> LbRows:
-    """Rows (tokens, heads, width), or (tokens, width) for one head, unit stride within a row."""
-    _tensor(t, device, name)
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2:
-        shape, stride = (shape[0], 1, shape[1]), (stride[0], 0, stride[1])
-    if len(shape) != 3 or stride[2] != 1 or (tokens is not None and shape[0] != tokens):
-        raise ValueError(f"{name} must be (tokens, heads, width) or (tokens, width) with unit stride in its rows and "
-                         f"{'any' if tokens is None else tokens} tokens, got {tuple(t.shape)}, strides {t.stride()}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    return LbRows(t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0, shape[1], shape[2])
-
-
-def _dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in lb._DTYPE:
-        raise ValueError(f"{name}: {t.dtype} is not supported")
-    return lb._DTYPE[t.dtype]
+    return torch.cuda.stream(stream)
 
 
 class Rotary:
@@ -137,14 +64,12 @@ class Rotary:
         if bands is not None and not original > 0:
             raise ValueError("bands: the original context must be positive")
         host = (ctypes.c_uint64 * max(rotary_dim // 2, 1))()
-        code = _lib.littlebit_rotary_phases(rotary_dim, base, factor, original, slow, fast, int(log_ramp), host)
-        if code:
-            raise lb.LittleBitError(code, "littlebit_rotary_phases")
+        lb._check(_phases(rotary_dim, base, factor, original, slow, fast, int(log_ramp), host),
+                  "littlebit_rotary_phases")
         self.rotary_dim, self.interleaved, self.scale = rotary_dim, bool(interleaved), float(scale)
         self.phases = torch.frombuffer(bytearray(host), dtype=torch.int64).to(device)
         self.device = self.phases.device
-        self._c = LbRotary(self.phases.data_ptr(), rotary_dim, int(self.interleaved), self.scale)
-        self._ref = ctypes.addressof(self._c)
+        self._h = _b.rotary(self.phases, rotary_dim, self.interleaved, self.scale)
 
 
 def rotate(xs: list, positions: torch.Tensor, rope: Rotary, outs: list | None = None, inverse: bool = False,
@@ -152,20 +77,10 @@ def rotate(xs: list, positions: torch.Tensor, rope: Rotary, outs: list | None = 
     """Rotated rows of up to eight tensors (tokens, heads, width), fp16, bf16 or
     fp32, one dtype, in one launch.  ``outs`` may be ``xs`` (in place).
     inverse turns back; with scale 1 that is also the gradient of the rotation."""
-    if not xs:
-        raise ValueError("xs must not be empty")
-    n, device, dtype = len(xs), rope.device, xs[0].dtype
-    tokens = positions.shape[0] if isinstance(positions, torch.Tensor) and positions.dim() == 1 else None
-    pos = _list(positions, device, "positions")
-    src = (LbRows * n)(*[_rows(x, device, f"xs[{i}]", tokens, dtype) for i, x in enumerate(xs)])
-    if outs is None:
-        with _making(stream):
-            outs = [torch.empty(x.shape, dtype=dtype, device=device) for x in xs]
-    elif len(outs) != n:
-        raise ValueError("outs must have as many tensors as xs")
-    dst = (LbRows * n)(*[_rows(x, device, f"outs[{i}]", tokens, dtype) for i, x in enumerate(outs)])
-    _call("littlebit_rotary", device, stream, src, dst, n, tokens, _dtype(xs[0], "xs"), pos, rope._ref, int(inverse))
-    return outs
+    if stream is not None:
+        with _on(stream, rope.device):
+            return _b.rotate(rope._h, xs, positions, outs, inverse)
+    return _b.rotate(rope._h, xs, positions, outs, inverse)
 
 
 class Cache:
@@ -177,33 +92,11 @@ class Cache:
     and refs (n_pages,) are int32; ``Cache.empty`` makes them all."""
 
     def __init__(self, planes: list, table: torch.Tensor, length: torch.Tensor, refs: torch.Tensor):
-        if not planes:
-            raise ValueError("a cache has at least one plane")
-        _tensor(planes[0], None, "planes[0]")
-        device = planes[0].device
-        if planes[0].dim() != 4:
-            raise ValueError("planes are (n_pages, heads, page_size, width)")
-        n_pages, _, page_size, _ = planes[0].shape
-        arr = (LbPlane * len(planes))()
-        for i, p in enumerate(planes):
-            _tensor(p, device, f"planes[{i}]")
-            if p.dim() != 4 or p.shape[0] != n_pages or p.shape[2] != page_size or p.stride(3) != 1:
-                raise ValueError(f"planes[{i}] must be ({n_pages}, heads, {page_size}, width) with unit stride in its "
-                                 f"rows, got {tuple(p.shape)}, strides {p.stride()}")
-            st = [p.stride(d) if p.shape[d] > 1 else 0 for d in (0, 1, 2)]
-            arr[i] = LbPlane(p.data_ptr(), st[0], st[1], st[2], p.shape[1], p.shape[3], _dtype(p, f"planes[{i}]"))
-        _tensor(table, device, "table")
-        if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1 and table.shape[1] > 1:
-            raise ValueError("table must be an int32 tensor (n_slots, max_pages) with unit stride in its rows")
-        n_slots, max_pages = table.shape
+        self._h = _b.cache(planes, table, length, refs)
         self.planes, self.table, self.length, self.refs = list(planes), table, length, refs
-        self.device, self.n_pages, self.page_size = device, n_pages, page_size
-        self.n_slots, self.max_pages = n_slots, max_pages
-        self._planes = arr
-        self._c = LbCache(arr, len(planes), n_pages, page_size, n_slots, max_pages,
-                          table.stride(0) if n_slots > 1 else max_pages, table.data_ptr(),
-                          _list(length, device, "length", n_slots), _list(refs, device, "refs", n_pages))
-        self._ref = ctypes.addressof(self._c)
+        self.device = table.device
+        self.n_pages, self.page_size = planes[0].shape[0], planes[0].shape[2]
+        self.n_slots, self.max_pages = table.shape
 
     @classmethod
     def empty(cls, shapes: list, n_pages: int, page_size: int, n_slots: int, max_pages: int, dtype=torch.float16,
@@ -215,72 +108,60 @@ class Cache:
                    torch.zeros(n_pages, dtype=torch.int32, device=device))
 
     # ---- bookkeeping
-    def _places(self, tokens: int, stream, out):
-        if out is not None:
-            where, positions = out
-        else:
-            with _making(stream):
-                where = torch.empty(tokens, dtype=torch.int64, device=self.device)
-                positions = torch.empty(tokens, dtype=torch.int32, device=self.device)
-        return (where, positions, _list(where, self.device, "where", tokens, torch.int64),
-                _list(positions, self.device, "positions", tokens))
-
     def extend(self, slots: torch.Tensor, starts: torch.Tensor, tokens: int, prefix: int = -1, out=None, stream=None):
         """Room for new tokens: slots[i] grows by starts[i+1] - starts[i].
         Returns (where, positions) of the step's ``tokens`` tokens: their rows
         in the cache (int64, -1: none) and their places in their sequences,
         behind slot ``prefix``'s tokens if it is given (int32)."""
-        n = slots.shape[0]
-        where, positions, w, p = self._places(tokens, stream, out)
-        _call("littlebit_cache_extend", self.device, stream, self._ref, _list(slots, self.device, "slots"),
-              _list(starts, self.device, "starts", n + 1), n, tokens, prefix, w, p)
-        return where, positions
+        if stream is not None:
+            with _on(stream, self.device):
+                return _b.extend(self._h, slots, starts, tokens, prefix, out)
+        return _b.extend(self._h, slots, starts, tokens, prefix, out)
 
     def locate(self, slots: torch.Tensor, starts: torch.Tensor, tokens: int, first: torch.Tensor | None = None,
                prefix: int = -1, out=None, stream=None):
         """(where, positions), as ``extend`` gives them, of tokens held: the
         tokens from first[i] (default 0) of slots[i] on."""
-        n = slots.shape[0]
-        where, positions, w, p = self._places(tokens, stream, out)
-        _call("littlebit_cache_locate", self.device, stream, self._ref, _list(slots, self.device, "slots"),
-              _list(starts, self.device, "starts", n + 1),
-              None if first is None else _list(first, self.device, "first", n), n, tokens, prefix, w, p)
-        return where, positions
+        if stream is not None:
+            with _on(stream, self.device):
+                return _b.locate(self._h, slots, starts, tokens, first, prefix, out)
+        return _b.locate(self._h, slots, starts, tokens, first, prefix, out)
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
         """Makes each (empty) slot children[i] a copy of slot parents[i]: full
         pages are shared, a partly filled last page is copied."""
-        n = parents.shape[0]
-        with _making(stream):
-            work = torch.empty(_lib.littlebit_cache_fork_work(n), dtype=torch.uint8, device=self.device)
-        _call("littlebit_cache_fork", self.device, stream, self._ref, _list(parents, self.device, "parents"),
-              _list(children, self.device, "children", n), n, work.data_ptr())
+        if stream is not None:
+            with _on(stream, self.device):
+                return _b.fork(self._h, parents, children)
+        return _b.fork(self._h, parents, children)
 
     def free(self, slots: torch.Tensor, stream=None) -> None:
         """Empties the slots; pages that no other slot holds become free."""
-        _call("littlebit_cache_free", self.device, stream, self._ref, _list(slots, self.device, "slots"),
-              slots.shape[0])
+        if stream is not None:
+            with _on(stream, self.device):
+                return _b.free(self._h, slots)
+        return _b.free(self._h, slots)
 
     def compact(self, into: bool = False, stream=None):
         """Moves the pages in use to the lowest numbers.  Returns (table, refs,
         count of pages in use): the cache's own tensors, updated, or with
         ``into`` new ones, the cache's staying as they are (and the rows they
         lead to good until a page is taken)."""
-        with _making(stream):
-            work = torch.empty(_lib.littlebit_cache_compact_work(self.n_pages), dtype=torch.uint8, device=self.device)
-            count = torch.empty(1, dtype=torch.int32, device=self.device)
-            table = torch.empty_strided(self.table.shape, self.table.stride(), dtype=torch.int32,
-                                        device=self.device) if into else self.table
-            refs = torch.empty_like(self.refs) if into else self.refs
-        _call("littlebit_cache_compact", self.device, stream, self._ref, table.data_ptr(), refs.data_ptr(),
-              count.data_ptr(), work.data_ptr())
-        return table, refs, count
+        if stream is not None:
+            with _on(stream, self.device):
+                return self.compact(into)
+        table, refs = self.table, self.refs
+        if into:
+            table, refs = torch.empty_strided(table.shape, table.stride(), dtype=torch.int32,
+                                              device=self.device), torch.empty_like(refs)
+        return table, refs, _b.compact(self._h, table, refs)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copies page src[i] to page dst[i] in every plane."""
-        n = src.shape[0]
-        _call("littlebit_cache_copy", self.device, stream, self._ref, _list(src, self.device, "src"),
-              _list(dst, self.device, "dst", n), n)
+        if stream is not None:
+            with _on(stream, self.device):
+                return _b.copy(self._h, src, dst)
+        return _b.copy(self._h, src, dst)
 
     # ---- rows
     def write(self, planes: list, rows: list, where: torch.Tensor, rope: Rotary | None = None,
@@ -290,57 +171,20 @@ class Cache:
         ``where``, one launch.  The planes whose place i is in ``rotated`` get
         their rows rotated by ``rope`` at ``positions``; q is rotated beside
         them and returned."""
-        n, tokens = len(planes), where.shape[0]
-        if n == 0 or len(rows) != n:
-            raise ValueError("planes and rows must be lists of the same length, not empty")
-        if (rotated or q is not None) and (rope is None or positions is None):
-            raise ValueError("rotating needs rope and positions")
-        if rope is not None and rope.device != self.device:
-            raise ValueError(f"rope is on {rope.device}, not {self.device}")
-        bits = 0
-        for i in rotated:
-            if not 0 <= i < n:
-                raise ValueError(f"rotated: {i} is not a place in planes")
-            bits |= 1 << i
-        dtype = rows[0].dtype
-        _dtype(rows[0], "rows")
-        src = (LbRows * n)(*[_rows(r, self.device, f"rows[{i}]", tokens, dtype) for i, r in enumerate(rows)])
-        qs = qd = None
-        if q is not None:
-            qs = ctypes.byref(_rows(q, self.device, "q", tokens, dtype))
-            if q_out is None:
-                with _making(stream):
-                    q_out = torch.empty(q.shape, dtype=dtype, device=self.device)
-            qd = ctypes.byref(_rows(q_out, self.device, "q_out", tokens, dtype))
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        for i in planes:
-            if not 0 <= i < len(self.planes) or self.planes[i].dtype != dtype:
-                raise ValueError(f"plane {i}: there is none, or its dtype is not the rows' {dtype}")
-        _call("littlebit_cache_write", self.device, stream, self._ref, (_I * n)(*planes), src, n, tokens,
-              _list(where, self.device, "where", None, torch.int64), None if rope is None else rope._ref,
-              None if positions is None else _list(positions, self.device, "positions", tokens), bits, qs, qd)
-        return q_out
+        h = None if rope is None else rope._h
+        if stream is not None:
+            with _on(stream, self.device):
+                return _b.write(self._h, planes, rows, where, h, positions, rotated, q, q_out)
+        return _b.write(self._h, planes, rows, where, h, positions, rotated, q, q_out)
 
     def read(self, planes: list, where: torch.Tensor, outs: list | None = None, stream=None) -> list:
         """The rows ``where`` of the planes, (tokens, heads, width) each; rows
         whose ``where`` is -1 are left as ``outs`` has them (undefined in
         tensors made here).  Up to eight planes of one dtype."""
-        n, tokens = len(planes), where.shape[0]
-        for i in planes:
-            if not 0 <= i < len(self.planes):
-                raise ValueError(f"there is no plane {i}")
-        if n == 0 or outs is not None and len(outs) != n:
-            raise ValueError("planes must not be empty, and outs as long")
-        dtype = self.planes[planes[0]].dtype
-        if outs is None:
-            with _making(stream):
-                outs = [torch.empty((tokens, self.planes[i].shape[1], self.planes[i].shape[3]),
-                                    dtype=self.planes[i].dtype, device=self.device) for i in planes]
-        dst = (LbRows * n)(*[_rows(r, self.device, f"outs[{i}]", tokens, dtype) for i, r in enumerate(outs)])
-        _call("littlebit_cache_read", self.device, stream, self._ref, (_I * n)(*planes), dst, n, tokens,
-              _list(where, self.device, "where", None, torch.int64))
-        return outs
+        if stream is not None:
+            with _on(stream, self.device):
+                return _b.read(self._h, planes, where, outs)
+        return _b.read(self._h, planes, where, outs)
 
     # ---- attention
     def attend(self, q: torch.Tensor, slots: torch.Tensor, starts: torch.Tensor, k: int = 0, v: int = 1,
@@ -354,18 +198,7 @@ class Cache:
         planes (fp16 or bf16, width 64 or 128).  scale: default width^-0.5.
         Rows in no sequence are left as ``out`` has them (undefined in one made
         here)."""
-        tokens, n = q.shape[0], slots.shape[0]
-        cq = _rows(q, self.device, "q", None, self.planes[k].dtype if 0 <= k < len(self.planes) else None)
-        if out is None:
-            with _making(stream):
-                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        co = _rows(out, self.device, "out", tokens, q.dtype)
-        if scale is None:
-            scale = 1.0 / math.sqrt(cq.width)
-        size = _lib.littlebit_cache_attend_work(self._ref, k, cq.heads, tokens, n, most_q, prefix >= 0)
-        with _making(stream):
-            work = torch.empty(size, dtype=torch.uint8, device=self.device)
-        _call("littlebit_cache_attend", self.device, stream, self._ref, k, v, ctypes.byref(cq), tokens,
-              _list(slots, self.device, "slots"), _list(starts, self.device, "starts", n + 1), n, prefix, most_q,
-              scale, ctypes.byref(co), work.data_ptr(), size)
-        return out
+        if stream is not None:
+            with _on(stream, self.device):
+                return _b.attend(self._h, q, slots, starts, k, v, prefix, most_q, scale, out)
+        return _b.attend(self._h, q, slots, starts, k, v, prefix, most_q, scale, out)

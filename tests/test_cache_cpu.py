@@ -12,12 +12,68 @@ from oracle import cache_oracle as orc
 ARG, ALIGN, SHAPE, UNSUPPORTED = 1, 2, 3, 6
 
 
+_P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+
+
+class _C:
+    """The C structures and entry points of include/littlebit.h."""
+
+    class LbPlane(ctypes.Structure):
+        _fields_ = [("data", _P), ("stride_page", _L), ("stride_head", _L), ("stride_row", _L), ("heads", _I),
+                    ("width", _I), ("dt", _I)]
+
+    class LbRows(ctypes.Structure):
+        _fields_ = [("data", _P), ("stride_token", _L), ("stride_head", _L), ("heads", _I), ("width", _I)]
+
+    class LbRotary(ctypes.Structure):
+        _fields_ = [("phases", _P), ("rotary_dim", _I), ("interleaved", _I), ("scale", ctypes.c_float)]
+
+
+class _LbCache(ctypes.Structure):
+    _fields_ = [("planes", ctypes.POINTER(_C.LbPlane)), ("n_planes", _I), ("n_pages", _I), ("page_size", _I),
+                ("n_slots", _I), ("max_pages", _I), ("table_stride", _L), ("table", _P), ("length", _P), ("refs", _P)]
+
+
+_C.LbCache = _LbCache
+_ARGS = {
+    "rotary_phases": [_I] + [ctypes.c_double] * 5 + [_I, _P],
+    "rotary": [_P, _P, _I, _I, _I, _P, _P, _I, _P],
+    "cache_extend": [_P, _P, _P, _I, _I, _I, _P, _P, _P],
+    "cache_locate": [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P],
+    "cache_write": [_P, _P, _P, _I, _I, _P, _P, _P, ctypes.c_uint, _P, _P, _P],
+    "cache_read": [_P, _P, _P, _I, _I, _P, _P],
+    "cache_fork": [_P, _P, _P, _I, _P, _P],
+    "cache_free": [_P, _P, _I, _P],
+    "cache_compact": [_P, _P, _P, _P, _P, _P],
+    "cache_copy": [_P, _P, _P, _I, _P],
+    "cache_attend": [_P, _I, _I, _P, _I, _P, _P, _I, _I, _I, ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
+    "cache_attend_work": [_P, _I, _I, _I, _I, _I, _I],
+}
+
+
 @pytest.fixture(scope="module")
 def cm():
     from latent_binary_factorization_b200 import build_ext
-    build_ext.build()
+    _C._lib = ctypes.CDLL(build_ext.build())
+    for name, args in _ARGS.items():
+        f = getattr(_C._lib, "littlebit_" + name)
+        f.argtypes, f.restype = args, ctypes.c_size_t if name.endswith("_work") else ctypes.c_int
+    return _C
+
+
+def test_the_python_module_imports_without_a_gpu(cm):
+    from latent_binary_factorization_b200 import build_ext
+    build_ext.build_binding()
+    import torch
     from latent_binary_factorization_b200 import cache
-    return cache
+    cpu = torch.zeros(1, 1, 8, 16, dtype=torch.float16)
+    ints = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        cache.Cache([cpu], ints.view(1, 1), ints, ints)
+    with pytest.raises(ValueError):
+        cache.Cache([], ints.view(1, 1), ints, ints)
+    with pytest.raises(ValueError):
+        cache.Rotary(16, bands=(0, 1, 2), device="cpu")
 
 
 def _cache(cm, dt=0, width=128, heads=8, page=16, **over):
