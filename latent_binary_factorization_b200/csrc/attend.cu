@@ -88,6 +88,7 @@ struct AttendArgs {
   Divisor by_group;
   float scale_log2;
   int do_prefix, do_own;       // which key sets this launch takes
+  int after_many;              // the launch before is many_rows_kernel of the same call
   PlanHead* head;              // written by block 0 for the join
   SeqPlan* seqs;
   float2* ml;                  // [partial][rows_alloc] maximum (times log2 e) and sum
@@ -159,20 +160,75 @@ struct Begin {
   int seq_segs;              // segments before it
 };
 
-// Run by the whole block (THREADS threads).  Two sweeps over the
-// sequences, THREADS at a time: the total, then the place of u0.  Block 0
-// leaves the plan for join_kernel.
+// Run by the whole block (THREADS threads): a sweep over the sequences, THREADS
+// at a time, for the total, and another for the place of u0, which a list that
+// fits one step need not take.  Block 0 leaves the plan for join_kernel.
 template <class C, int THREADS>
 __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ long long warp_u[W];
+  __shared__ int warp_s[W], found[3];   // sequence, units before, segments before
   Begin b;
-  b.t0 = min(max(a.starts[0], 0), a.n_tokens);
-  const int t1 = min(max(a.starts[a.n], b.t0), a.n_tokens);
+  long long p_units = 0, u = 0;         // the sums are taken in 64 bits, and used if they fit 31
+  int segs = 0;
+  // this thread's sequence of the step: its units, and those and the segments before it
+  long long mine = 0, before_u = 0;
+  int before_s = 0;
+  auto step = [&](int i0, bool leave) {
+    const int i = i0 + tid;
+    int mine_s = 0, head = 0;
+    Seq s{};
+    mine = 0;
+    if (i < a.n) {
+      s = load_seq(a, i);
+      const int rows = s.count * a.group;
+      mine_s = up_div(rows, C::kRows) * a.heads;
+      head = own_head<C>(a.by_group, rows, s.len, s.before);
+      mine = (long long)head * a.heads;
+      if (leave && s.slot != -1 && (s.slot < 0 || s.slot >= a.n_slots)) atomicOr(a.status, kStatusIndex);
+    }
+    long long xu = mine;
+    int xs = mine_s;
+#pragma unroll 1
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long yu = __shfl_up_sync(0xffffffffu, xu, d);
+      const int ys = __shfl_up_sync(0xffffffffu, xs, d);
+      if (lane >= d) {
+        xu += yu;
+        xs += ys;
+      }
+    }
+    __syncthreads();
+    if (lane == 31) {
+      warp_u[warp] = xu;
+      warp_s[warp] = xs;
+    }
+    __syncthreads();
+    before_u = u + xu - mine;
+    before_s = segs + xs - mine_s;
+#pragma unroll 1
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) {
+        before_u += warp_u[w];
+        before_s += warp_s[w];
+      }
+      u += warp_u[w];
+      segs += warp_s[w];
+    }
+    if (leave && i < a.n)
+      a.seqs[i] = SeqPlan{(int)min(before_u, (long long)kMaxUnits), before_s, s.first, s.count, s.len, s.before, head, 0};
+  };
+
+  // everything that depends on nothing is asked for before the first use of any of it
+  const int start0 = a.starts[0], start_n = a.starts[a.n], p_len = a.do_prefix ? a.length[a.prefix] : 0;
+  const int warm = a.do_own && tid < a.n ? a.slots[tid] + a.starts[tid] + a.starts[tid + 1] : 0;
+  asm volatile("" ::"r"(start0), "r"(start_n), "r"(p_len), "r"(warm));
+  b.t0 = min(max(start0, 0), a.n_tokens);
+  const int t1 = min(max(start_n, b.t0), a.n_tokens);
   b.p_rows = b.p_rt = b.p_kt = b.p_len = 0;
-  long long p_units = 0;   // the sums are taken in 64 bits, and used if they fit 31
   if (a.do_prefix) {
-    b.p_len = min(max(a.length[a.prefix], 0), a.max_pages << a.page_shift);
+    b.p_len = min(max(p_len, 0), a.max_pages << a.page_shift);
     b.p_rows = (t1 - b.t0) * a.group;
     b.p_rt = up_div(b.p_rows, C::kRows);
     b.p_kt = up_div(b.p_len, C::kKeys);
@@ -181,90 +237,39 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
   }
   b.p_head = (int)min(p_units, (long long)kMaxUnits);
   p_units *= a.heads;
-  const int p_segs = b.p_rt * a.heads;
-  __shared__ long long warp_u[W];
-  __shared__ int warp_s[W], found[3];   // sequence, units before, segments before
-  long long total = p_units;
+  const int p_segs = b.p_rt * a.heads, n = a.do_own ? a.n : 0;
+  u = p_units;
+  segs = p_segs;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 1) {
-      // every block but the last ones has the same number of units; a block inside a segment always has some
-      const bool fits = total <= kMaxUnits - 1024 * 1024;
-      const int width = fits ? max(((int)total + (int)gridDim.x - 1) / (int)gridDim.x, 1) : 0;
-      b.u0 = (int)min((long long)width * blockIdx.x, total);
-      b.u1 = (int)min((long long)width * (blockIdx.x + 1), total);
-      b.seq = -1;
-      b.seq_u = 0;
-      b.seq_segs = 0;
-      if (blockIdx.x == 0 && tid == 0) {
-        *a.head = PlanHead{width, b.t0, t1, b.p_rows, b.p_rt, b.p_kt, b.p_head, 0};
-        if (!fits) atomicOr(a.status, kStatusIndex);
-      }
-      if (b.u0 < p_units || b.u0 >= b.u1) break;
-    }
-    long long u = p_units;
-    int segs = p_segs;
-    if (a.do_own)
+  for (int i0 = 0; i0 < n; i0 += THREADS) step(i0, blockIdx.x == 0);
+
+  // every block but the last ones has the same number of units; a block inside a segment always has some
+  const bool fits = u <= kMaxUnits - 1024 * 1024;
+  const int width = fits ? max(((int)u + (int)gridDim.x - 1) / (int)gridDim.x, 1) : 0;
+  b.u0 = (int)min((long long)width * blockIdx.x, u);
+  b.u1 = (int)min((long long)width * (blockIdx.x + 1), u);
+  b.seq = -1;
+  b.seq_u = b.seq_segs = 0;
+  if (blockIdx.x == 0 && tid == 0) {
+    *a.head = PlanHead{width, b.t0, t1, b.p_rows, b.p_rt, b.p_kt, b.p_head, 0};
+    if (!fits) atomicOr(a.status, kStatusIndex);
+  }
+  if (b.u0 < p_units || b.u0 >= b.u1) return b;
+  u = p_units;
+  segs = p_segs;
 #pragma unroll 1
-      for (int i0 = 0; i0 < a.n; i0 += THREADS) {
-        const int i = i0 + tid;
-        long long mine = 0;
-        int mine_s = 0, head = 0;
-        Seq s{};
-        if (i < a.n) {
-          s = load_seq(a, i);
-          const int rows = s.count * a.group;
-          mine_s = up_div(rows, C::kRows) * a.heads;
-          head = own_head<C>(a.by_group, rows, s.len, s.before);
-          mine = (long long)head * a.heads;
-          if (s.slot != -1 && (s.slot < 0 || s.slot >= a.n_slots) && blockIdx.x == 0)
-            atomicOr(a.status, kStatusIndex);
-        }
-        long long xu = mine;
-        int xs = mine_s;
-#pragma unroll 1
-        for (int d = 1; d < 32; d <<= 1) {
-          const long long yu = __shfl_up_sync(0xffffffffu, xu, d);
-          const int ys = __shfl_up_sync(0xffffffffu, xs, d);
-          if (lane >= d) {
-            xu += yu;
-            xs += ys;
-          }
-        }
-        __syncthreads();
-        if (lane == 31) {
-          warp_u[warp] = xu;
-          warp_s[warp] = xs;
-        }
-        __syncthreads();
-        long long before_u = u + xu - mine;
-        int before_s = segs + xs - mine_s;
-#pragma unroll 1
-        for (int w = 0; w < W; ++w) {
-          if (w < warp) {
-            before_u += warp_u[w];
-            before_s += warp_s[w];
-          }
-          u += warp_u[w];
-          segs += warp_s[w];
-        }
-        if (pass == 0) {
-          if (blockIdx.x == 0 && i < a.n)
-            a.seqs[i] = SeqPlan{(int)min(before_u, (long long)kMaxUnits), before_s, s.first, s.count, s.len, s.before, head, 0};
-        } else if (b.u0 >= before_u && b.u0 < before_u + mine) {
-          found[0] = i;
-          found[1] = (int)before_u;
-          found[2] = before_s;
-        }
-      }
-    total = u;
-    if (pass == 1) {
-      __syncthreads();
-      b.seq = found[0];
-      b.seq_u = found[1];
-      b.seq_segs = found[2];
+  for (int i0 = 0; i0 < n; i0 += THREADS) {
+    if (n > THREADS) step(i0, false);
+    if (b.u0 >= before_u && b.u0 < before_u + mine) {
+      found[0] = i0 + tid;
+      found[1] = (int)before_u;
+      found[2] = before_s;
     }
   }
+  __syncthreads();
+  b.seq = found[0];
+  b.seq_u = found[1];
+  b.seq_segs = found[2];
   return b;
 }
 
@@ -436,14 +441,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   __shared__ float2 stat[4][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
+  // Behind a launch of many_rows_kernel nothing of that one is needed here (it began after all work before it was
+  // done), so blocks start as its blocks leave; but the join needs both done, hence the wait at the end.
+  if (a.after_many) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  else lb::dependent_begin();
   const Begin b = plan_block<FewCut, kFewThreads>(a);
-  if (b.u0 >= b.u1) return;
+  if (b.u0 >= b.u1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const uint32_t ring = shared_addr(smem) + warp * S * kFewStage<D>;
   float* joined = reinterpret_cast<float*>(smem + 4 * S * kFewStage<D>);
 
   // ---- loads: page numbers one tile ahead of the copies, copies S - 1 tiles ahead of the products
   Piece<FewCut> lp;
   lp.begin(a, b);
+  Piece<FewCut> w = lp;   // the piece that is computed
   int lt = lp.t0;   // next tile to copy
   bool more = true;
   int page[2] = {0, 0};
@@ -485,109 +498,121 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll 1
-  for (int s = 0; s < S - 1; ++s) issue(s);
-
-  Piece<FewCut> w;
-  w.begin(a, b);
+  // ---- products
   uint32_t qf[D / 16][4];
   float o[D / 8][4];
   float m[2], l[2];
   int lim[2];   // keys that rows g and g + 8 see
-  int stage = 0;
-  do {
-    const int slot = w.seg + (int)blockIdx.x;
-    const int rows = slot < a.n_partials ? min(min(kFewRows, a.rows_alloc), w.rows_left()) : 0;
-    if (w.t0 == w.t1) {   // units of the segment's beginning only
-      if (threadIdx.x < rows) a.ml[(long long)slot * a.rows_alloc + threadIdx.x] = make_float2(-INFINITY, 0.f);
-      continue;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = w.r * kFewRows + g + 8 * i;
-      const int tok = a.by_group(row);
-      const bool in = row < w.rows;
-      lim[i] = in ? w.sees(tok) : 0;
-      const unsigned char* src =
-          a.q + (long long)(w.first + tok) * a.q_token + (long long)(w.h * a.group + row - tok * a.group) * a.q_head;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[k][i] = in ? *reinterpret_cast<const uint32_t*>(src + k * 32 + c * 4) : 0;
-        qf[k][i + 2] = in ? *reinterpret_cast<const uint32_t*>(src + k * 32 + 16 + c * 4) : 0;
+  int stage = 0, ahead = 0, t = 0;      // ahead: copies begun, up to S - 1
+  int slot = 0, rows = 0;
+  bool fresh = true, begun = false;     // fresh: a new piece
+  for (;;) {
+    if (fresh) {
+      fresh = false;
+#pragma unroll 1
+      for (;;) {
+        if (begun && !w.next(a)) goto done;
+        begun = true;
+        slot = w.seg + (int)blockIdx.x;
+        rows = slot < a.n_partials ? min(min(kFewRows, a.rows_alloc), w.rows_left()) : 0;
+        if (w.t0 < w.t1) break;
+        // units of the segment's beginning only
+        if (threadIdx.x < rows) a.ml[(long long)slot * a.rows_alloc + threadIdx.x] = make_float2(-INFINITY, 0.f);
       }
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-    }
+      t = w.t0;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    for (int t = w.t0; t < w.t1; ++t) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-      __syncwarp();
-      issue(stage == 0 ? S - 1 : stage - 1);
-      const int key = t * kFewKeys + 16 * warp;
-      if (key < w.len) {
-        const uint32_t kb = ring + stage * kFewStage<D>, vb = kb + 32 * D;
-        float s[2][4] = {};
+      for (int i = 0; i < 2; ++i) {
+        const int row = w.r * kFewRows + g + 8 * i;
+        const int tok = a.by_group(row);
+        const bool in = row < w.rows;
+        lim[i] = in ? w.sees(tok) : 0;
+        const unsigned char* src =
+            a.q + (long long)(w.first + tok) * a.q_token + (long long)(w.h * a.group + row - tok * a.group) * a.q_head;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          uint32_t f[4];
-          const int row = ((lane >> 4) << 3) + (lane & 7), ch = 2 * k + ((lane >> 3) & 1);
-          ldmatrix4<false>(f, kb + row * (2 * D) + ((ch ^ (row & 7)) << 4));
-          Mma<T>::run(s[0], qf[k], f[0], f[1]);
-          Mma<T>::run(s[1], qf[k], f[2], f[3]);
+          qf[k][i] = in ? *reinterpret_cast<const uint32_t*>(src + k * 32 + c * 4) : 0;
+          qf[k][i + 2] = in ? *reinterpret_cast<const uint32_t*>(src + k * 32 + 16 + c * 4) : 0;
         }
-        // scores in units of log 2; keys a row does not see get -inf
-        float top[2] = {-INFINITY, -INFINITY};
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    }
+    if (ahead == S - 1) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+      __syncwarp();
+    }
+    // the one place that copies; the first S - 1 rounds do nothing else
+    issue(ahead < S - 1 ? ahead : stage == 0 ? S - 1 : stage - 1);
+    if (ahead < S - 1) {
+      ++ahead;
+      continue;
+    }
+    const int key = t * kFewKeys + 16 * warp;
+    if (key < w.len) {
+      const uint32_t kb = ring + stage * kFewStage<D>, vb = kb + 32 * D;
+      float s[2][4] = {};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at = key + 8 * n + 2 * c + (e & 1);
-            s[n][e] = at < lim[e >> 1] ? s[n][e] * a.scale_log2 : -INFINITY;
-            top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
-          }
-        float alpha[2], base[2];
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t f[4];
+        const int row = ((lane >> 4) << 3) + (lane & 7), ch = 2 * k + ((lane >> 3) & 1);
+        ldmatrix4<false>(f, kb + row * (2 * D) + ((ch ^ (row & 7)) << 4));
+        Mma<T>::run(s[0], qf[k], f[0], f[1]);
+        Mma<T>::run(s[1], qf[k], f[2], f[3]);
+      }
+      // scores in units of log 2; keys a row does not see get -inf
+      float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-          const float now = fmaxf(m[i], top[i]);
-          base[i] = now == -INFINITY ? 0.f : now;
-          alpha[i] = exp2_fast(m[i] - base[i]);
-          m[i] = now;
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = key + 8 * n + 2 * c + (e & 1);
+          s[n][e] = at < lim[e >> 1] ? s[n][e] * a.scale_log2 : -INFINITY;
+          top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
         }
-        float sum[2] = {0.f, 0.f};
+      float alpha[2], base[2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int i = 0; i < 2; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        const float now = fmaxf(m[i], top[i]);
+        base[i] = now == -INFINITY ? 0.f : now;
+        alpha[i] = exp2_fast(m[i] - base[i]);
+        m[i] = now;
+      }
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[n][e] = exp2_fast(s[n][e] - base[e >> 1]);
-            sum[e >> 1] += s[n][e];
-          }
-        l[0] = l[0] * alpha[0] + sum[0];
-        l[1] = l[1] * alpha[1] + sum[1];
-        const uint32_t p[4] = {Mma<T>::pack(s[0][0], s[0][1]), Mma<T>::pack(s[0][2], s[0][3]),
-                               Mma<T>::pack(s[1][0], s[1][1]), Mma<T>::pack(s[1][2], s[1][3])};
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= alpha[0];
-            o[i][1] *= alpha[0];
-            o[i][2] *= alpha[1];
-            o[i][3] *= alpha[1];
-          }
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = exp2_fast(s[n][e] - base[e >> 1]);
+          sum[e >> 1] += s[n][e];
         }
+      l[0] = l[0] * alpha[0] + sum[0];
+      l[1] = l[1] * alpha[1] + sum[1];
+      const uint32_t p[4] = {Mma<T>::pack(s[0][0], s[0][1]), Mma<T>::pack(s[0][2], s[0][3]),
+                             Mma<T>::pack(s[1][0], s[1][1]), Mma<T>::pack(s[1][2], s[1][3])};
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          uint32_t f[4];
-          const int row = lane & 15, ch = 2 * d + (lane >> 4);
-          ldmatrix4<true>(f, vb + row * (2 * D) + ((ch ^ (row & 7)) << 4));
-          Mma<T>::run(o[2 * d], p, f[0], f[1]);
-          Mma<T>::run(o[2 * d + 1], p, f[2], f[3]);
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1];
+          o[i][3] *= alpha[1];
         }
       }
-      stage = stage + 1 == S ? 0 : stage + 1;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        uint32_t f[4];
+        const int row = lane & 15, ch = 2 * d + (lane >> 4);
+        ldmatrix4<true>(f, vb + row * (2 * D) + ((ch ^ (row & 7)) << 4));
+        Mma<T>::run(o[2 * d], p, f[0], f[1]);
+        Mma<T>::run(o[2 * d + 1], p, f[2], f[3]);
+      }
     }
+    stage = stage + 1 == S ? 0 : stage + 1;
+    if (++t < w.t1) continue;
     // ---- join the four warps' partials and write the segment's
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -641,8 +666,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       }
       __syncthreads();
     }
-  } while (w.next(a));
+    fresh = true;
+  }
+done:
   if (bad) atomicOr(a.status, bad);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ many rows
@@ -889,6 +917,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __shared__ volatile uint32_t loads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  lb::dependent_begin();
   const Begin b = plan_block<ManyCut, kManyThreads>(a);
   if (b.u0 >= b.u1) return;   // the whole block
   if (warp == 9) {
@@ -1241,7 +1270,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   constexpr int E = D / 32;
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  lb::dependent_begin();
   __shared__ int s_seq;
   if (threadIdx.x == 0) s_seq = -1;
   __syncthreads();
@@ -1458,18 +1487,16 @@ cudaError_t launch(const Split& s, const AttendArgs& few, const AttendArgs& many
   if (s.many.blocks) {
     e = allow_smem(many_rows_kernel<T, D>, many_smem, kManySmem<D>);
     if (e != cudaSuccess) return e;
-    many_rows_kernel<T, D><<<s.many.blocks, kManyThreads, kManySmem<D>, st>>>(many, k, v);
-    e = cudaGetLastError();
+    e = lb::launch_dependent_on(st, many_rows_kernel<T, D>, dim3(s.many.blocks), kManyThreads, kManySmem<D>, many, k, v);
   }
   if (e == cudaSuccess && s.few.blocks) {
     e = allow_smem(few_rows_kernel<T, D>, few_smem, kFewSmem<D>);
     if (e != cudaSuccess) return e;
-    few_rows_kernel<T, D><<<s.few.blocks, kFewThreads, kFewSmem<D>, st>>>(few);
-    e = cudaGetLastError();
+    e = lb::launch_dependent_on(st, few_rows_kernel<T, D>, dim3(s.few.blocks), kFewThreads, kFewSmem<D>, few);
   }
   if (e != cudaSuccess) return e;
-  join_kernel<T, D><<<dim3(join.n_tokens, lb::ceil_div(join.heads * join.group, 8)), 256, 0, st>>>(join);
-  return cudaGetLastError();
+  return lb::launch_dependent_on(st, join_kernel<T, D>, dim3(join.n_tokens, lb::ceil_div(join.heads * join.group, 8)),
+                                 256, 0, join);
 }
 
 lb_status check_attend(const lb_cache* c, int k, int heads_q, int n_tokens, int n, int most_q) {
@@ -1567,7 +1594,8 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
     return x;
   };
   unsigned char* w = static_cast<unsigned char*>(work);
-  const AttendArgs few = place(s.few, w, s.few_own, s.few_prefix);
+  AttendArgs few = place(s.few, w, s.few_own, s.few_prefix);
+  few.after_many = s.many.blocks > 0;
   const AttendArgs many = place(s.many, w + s.few.bytes, s.many_own, s.many_prefix);
   j.out = static_cast<unsigned char*>(out->data);
   j.out_token = 2 * out->stride_token;

@@ -39,10 +39,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 int elem_bytes(lb_dtype dt) { return dt == LB_F32 ? 4 : dt == LB_I8 ? 1 : 2; }
 
-lb_status launched() {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? LB_OK : lb::cuda_fail(e);
-}
+lb_status launched(cudaError_t e) { return e == cudaSuccess ? LB_OK : lb::cuda_fail(e); }
 
 // ------------------------------------------------------------------ rows
 
@@ -115,6 +112,7 @@ template <class T>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowArgs a) {
   constexpr int E = 16 / sizeof(T);
   extern __shared__ float2 turn[];   // [per_block][half]
+  lb::dependent_begin();
   const int t0 = blockIdx.x * a.per_block;
   const int n_tok = min(a.per_block, a.n_tokens - t0);
   const unsigned total = a.items * (unsigned)n_tok;
@@ -319,6 +317,7 @@ __global__ void __launch_bounds__(kBookThreads, 1)
   int* s_slot = s_off + n;        // [n]
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
+  lb::dependent_begin();
   for (int i = tid; i <= n; i += kBookThreads) s_start[i] = starts[i];
   __syncthreads();
   auto count = [&](int i) {
@@ -421,6 +420,7 @@ __global__ void __launch_bounds__(256)
     locate_kernel(const Tables c, const int* __restrict__ slots, const int* __restrict__ starts,
                   const int* __restrict__ begin, int n, int n_tokens, int prefix, long long* __restrict__ where,
                   int* __restrict__ positions) {
+  lb::dependent_begin();
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= n_tokens) return;
   int first;
@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(128) free_kernel(const Tables c, const int* __restrict__ slots) {
+  lb::dependent_begin();
   const int s = slots[blockIdx.x];
   if (s < 0 || s >= c.n_slots) {
     if (s != -1 && threadIdx.x == 0) atomicOr(&g_status, kStatusIndex);
@@ -544,6 +545,7 @@ __global__ void __launch_bounds__(kBookThreads, 1)
   int* s_child = s_off + n;   // [n]
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
+  lb::dependent_begin();
   unsigned bad = 0;
   for (int i = tid; i < n; i += kBookThreads) {
     const int p = parents[i], ch = children[i];
@@ -608,6 +610,7 @@ __global__ void __launch_bounds__(kBookThreads, 1)
 __global__ void __launch_bounds__(256)
     fork_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, const ForkJob* __restrict__ fork,
                      const CopyJob* __restrict__ copy, int n, int with_tables) {
+  lb::dependent_begin();
   if (with_tables && blockIdx.y == 0)
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
       const ForkJob f = fork[i];
@@ -630,6 +633,7 @@ __global__ void __launch_bounds__(kBookThreads, 1)
                    int* __restrict__ moved, int* __restrict__ n_jobs) {
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
+  lb::dependent_begin();
   int live = 0;
   for (int p = tid; p < c.n_pages; p += kBookThreads) live += c.refs[p] > 0;
   int count;
@@ -684,6 +688,7 @@ __global__ void __launch_bounds__(256)
     compact_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, int* table_out,
                         const int* __restrict__ count, const CopyJob* __restrict__ jobs,
                         const int* __restrict__ moved, const int* __restrict__ n_jobs, int with_tables) {
+  lb::dependent_begin();
   if (with_tables) {
     const int live = *count;
     const long long n = (long long)c.n_slots * c.max_pages;
@@ -700,6 +705,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     copy_kernel(const __grid_constant__ CopyArgs a, const int* __restrict__ src, const int* __restrict__ dst, int n,
                 int n_pages) {
+  lb::dependent_begin();
   copy_items(a, n, [&](int i) {
     CopyJob j{src[i], dst[i], a.page_size, 0};
     if (j.src == -1 && j.dst == -1) return j;   // padding
@@ -789,8 +795,8 @@ lb_status launch_rows_of(const RowArgs& a, cudaStream_t st) {
   // blocks that share a token's items: enough for four blocks an SM, none without work
   const int64_t need = ((int64_t)a.items * a.per_block + 255) / 256;
   const int y = (int)std::min<int64_t>(std::min<int64_t>(need, 1024), std::max(1, 148 * 4 / x));
-  rows_kernel<T><<<dim3(x, y), 256, (size_t)a.per_block * a.half * sizeof(float2), st>>>(a);
-  return launched();
+  return launched(lb::launch_dependent_on(st, rows_kernel<T>, dim3(x, y), 256,
+                                          (size_t)a.per_block * a.half * sizeof(float2), a));
 }
 
 // Fills and launches rows_kernel.
@@ -955,9 +961,9 @@ lb_status littlebit_cache_extend(const lb_cache* c, const int32_t* slots, const 
   cudaError_t e = lb::touch_cache_status(nullptr);
   if (e == cudaSuccess) e = allow_smem(extend_kernel, smem, most);
   if (e != cudaSuccess) return lb::cuda_fail(e);
-  extend_kernel<<<1, kBookThreads, (4 * n + 1) * sizeof(int), static_cast<cudaStream_t>(stream)>>>(
-      tables_of(*c), slots, starts, n, n_tokens, prefix, reinterpret_cast<long long*>(where), positions);
-  return launched();
+  return launched(lb::launch_dependent_on(static_cast<cudaStream_t>(stream), extend_kernel, dim3(1), kBookThreads,
+                                          (4 * n + 1) * sizeof(int), tables_of(*c), slots, starts, n, n_tokens, prefix,
+                                          reinterpret_cast<long long*>(where), positions));
 }
 
 lb_status littlebit_cache_locate(const lb_cache* c, const int32_t* slots, const int32_t* starts, const int32_t* first,
@@ -968,9 +974,9 @@ lb_status littlebit_cache_locate(const lb_cache* c, const int32_t* slots, const 
   if (!where || !positions) return LB_ERR_ARG;
   const cudaError_t e = lb::touch_cache_status(nullptr);
   if (e != cudaSuccess) return lb::cuda_fail(e);
-  locate_kernel<<<lb::ceil_div(n_tokens, 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-      tables_of(*c), slots, starts, first, n, n_tokens, prefix, reinterpret_cast<long long*>(where), positions);
-  return launched();
+  return launched(lb::launch_dependent_on(static_cast<cudaStream_t>(stream), locate_kernel,
+                                          dim3(lb::ceil_div(n_tokens, 256)), 256, 0, tables_of(*c), slots, starts,
+                                          first, n, n_tokens, prefix, reinterpret_cast<long long*>(where), positions));
 }
 
 lb_status littlebit_cache_write(const lb_cache* c, const int* planes, const lb_rows* rows, int n, int n_tokens,
@@ -1037,8 +1043,8 @@ lb_status littlebit_cache_free(const lb_cache* c, const int32_t* slots, int n, v
   if (n < 1 || n > kMaxList) return LB_ERR_SHAPE;
   const cudaError_t e = lb::touch_cache_status(nullptr);
   if (e != cudaSuccess) return lb::cuda_fail(e);
-  free_kernel<<<n, 128, 0, static_cast<cudaStream_t>(stream)>>>(tables_of(*c), slots);
-  return launched();
+  return launched(lb::launch_dependent_on(static_cast<cudaStream_t>(stream), free_kernel, dim3(n), 128, 0,
+                                          tables_of(*c), slots));
 }
 
 size_t littlebit_cache_fork_work(int n) {
@@ -1061,12 +1067,14 @@ lb_status littlebit_cache_fork(const lb_cache* c, const int32_t* parents, const 
   cudaError_t e = lb::touch_cache_status(nullptr);
   if (e == cudaSuccess) e = allow_smem(fork_kernel, smem, 3 * kMaxList * (int)sizeof(int));
   if (e != cudaSuccess) return lb::cuda_fail(e);
-  fork_kernel<<<1, kBookThreads, 3 * n * sizeof(int), st>>>(tables_of(*c), parents, children, n, fork, copy);
-  if ((r = launched()) != LB_OK) return r;
+  r = launched(lb::launch_dependent_on(st, fork_kernel, dim3(1), kBookThreads, 3 * n * sizeof(int), tables_of(*c),
+                                       parents, children, n, fork, copy));
+  if (r != LB_OK) return r;
   for (int b = 0; b < c->n_planes; b += kPlaneBatch) {
     const CopyArgs a = planes_of(*c, b);
-    fork_copy_kernel<<<copy_grid(a, n, c->page_size), 256, 0, st>>>(a, tables_of(*c), fork, copy, n, b == 0);
-    if ((r = launched()) != LB_OK) return r;
+    r = launched(lb::launch_dependent_on(st, fork_copy_kernel, copy_grid(a, n, c->page_size), 256, 0, a, tables_of(*c),
+                                         fork, copy, n, b == 0));
+    if (r != LB_OK) return r;
   }
   return LB_OK;
 }
@@ -1091,13 +1099,14 @@ lb_status littlebit_cache_compact(const lb_cache* c, int32_t* table_out, int32_t
   int* moved = reinterpret_cast<int*>(jobs + most + 1);
   const cudaError_t e = lb::touch_cache_status(nullptr);
   if (e != cudaSuccess) return lb::cuda_fail(e);
-  compact_kernel<<<1, kBookThreads, 0, st>>>(tables_of(*c), refs_out, count, jobs, moved, n_jobs);
-  if ((r = launched()) != LB_OK) return r;
+  r = launched(lb::launch_dependent_on(st, compact_kernel, dim3(1), kBookThreads, 0, tables_of(*c), refs_out, count,
+                                       jobs, moved, n_jobs));
+  if (r != LB_OK) return r;
   for (int b = 0; b < c->n_planes; b += kPlaneBatch) {
     const CopyArgs a = planes_of(*c, b);
-    compact_copy_kernel<<<copy_grid(a, std::max(most, 1), c->page_size), 256, 0, st>>>(
-        a, tables_of(*c), table_out, count, jobs, moved, n_jobs, b == 0);
-    if ((r = launched()) != LB_OK) return r;
+    r = launched(lb::launch_dependent_on(st, compact_copy_kernel, copy_grid(a, std::max(most, 1), c->page_size), 256, 0,
+                                         a, tables_of(*c), table_out, count, jobs, moved, n_jobs, b == 0));
+    if (r != LB_OK) return r;
   }
   return LB_OK;
 }
@@ -1113,9 +1122,9 @@ lb_status littlebit_cache_copy(const lb_cache* c, const int32_t* src, const int3
   if (e != cudaSuccess) return lb::cuda_fail(e);
   for (int b = 0; b < c->n_planes; b += kPlaneBatch) {
     const CopyArgs a = planes_of(*c, b);
-    copy_kernel<<<copy_grid(a, n, c->page_size), 256, 0, static_cast<cudaStream_t>(stream)>>>(a, src, dst, n,
-                                                                                             c->n_pages);
-    if ((r = launched()) != LB_OK) return r;
+    r = launched(lb::launch_dependent_on(static_cast<cudaStream_t>(stream), copy_kernel, copy_grid(a, n, c->page_size),
+                                         256, 0, a, src, dst, n, c->n_pages));
+    if (r != LB_OK) return r;
   }
   return LB_OK;
 }

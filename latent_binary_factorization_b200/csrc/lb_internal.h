@@ -244,6 +244,31 @@ size_t path_scratch_bytes(const lb_layer& L, int batch);
 // device `dev`, or null before that entry point's first call on the device.
 unsigned int* noalloc_status_word(int dev);
 
+// Programmatic dependent launch of the paged cache's kernels: each may be
+// scheduled while the stream's previous kernel ends, and waits for that one's
+// writes before it touches memory.  Every one of them calls dependent_begin()
+// first, so that its end implies the end of all work before it.
+#ifdef __CUDACC__
+__device__ __forceinline__ void dependent_begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch_dependent_on(cudaStream_t st, void (*kern)(P...), dim3 grid, int block, size_t smem, A&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+#endif
+
 // cache.cu: argument checks shared with attend.cu, and the status word of the
 // paged cache's calls (null before the first of them on the device).
 lb_status check_cache(const lb_cache* c);
