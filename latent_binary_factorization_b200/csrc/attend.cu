@@ -1264,53 +1264,62 @@ struct JoinArgs {
 };
 
 // One warp per (token, query head): finds the token's sequence, weighs the
-// row's partials of both key sets and writes the output.
+// row's partials of both key sets and writes the output.  Bound by latency at
+// decode sizes: the plan is one round of loads, the first four partials another.
 template <class T, int D>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int E = D / 32;
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
-  lb::dependent_begin();
-  __shared__ int s_seq;
-  if (threadIdx.x == 0) s_seq = -1;
+  __shared__ SeqPlan s_plan;
+  __shared__ int s_found;
+  if (threadIdx.x == 0) s_found = 0;
   __syncthreads();
+  lb::dependent_begin();
+  PlanHead head[2];
+  head[0] = *a.set[0].head;
+  head[1] = a.set[1].head ? *a.set[1].head : PlanHead{1, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
   for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
-    const int first = a.set[0].seqs[i].first, count = a.set[0].seqs[i].count;
-    if (t >= first && t < first + count) s_seq = i;
+    const SeqPlan s = a.set[0].seqs[i];
+    if (t >= s.first && t < s.first + s.count) {
+      s_plan = s;
+      s_found = 1;
+    }
   }
   __syncthreads();
-  const int seq = s_seq;
-  if (seq < 0 || h >= a.heads * a.group) return;
+  if (!s_found || h >= a.heads * a.group || head[0].width == 0 || head[1].width == 0) return;
+  const SeqPlan s = s_plan;
   const int kv = a.by_group(h), sub = h - kv * a.group;
-  float acc[E] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const Source& S = a.set[which];
+
+  // partials first[w], first[w] + step[w], ... (count[w] of them) of key set w, row row[w] of each
+  int first[2] = {0, 0}, step[2] = {1, 1}, count[2] = {0, 0}, at[2] = {0, 0};
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const Source& S = a.set[w];
     if (!S.head) continue;
-    const PlanHead H = *S.head;
-    if (H.width == 0) return;
-    // the row's segment: units ua .. ua + ext - 1
-    const int tile = S.few ? FewCut::kRows : ManyCut::kRows;
+    const bool few = S.few;
+    const int tile = few ? FewCut::kRows : ManyCut::kRows;
     auto extent_of = [&](int tiles, int left) {
-      return S.few ? extent<FewCut>(tiles, left) : extent<ManyCut>(tiles, left);
+      return few ? extent<FewCut>(tiles, left) : extent<ManyCut>(tiles, left);
     };
+    // the row's segment: units ua .. ua + ext - 1
     int row, left, r, ua, ext, seg;
-    if (which) {
-      row = (t - H.t0) * a.group + sub;
-      r = row / (unsigned)tile;
-      left = H.p_rows - r * tile;
-      ua = kv * H.p_head + r * extent_of(H.p_kt, tile);
-      ext = extent_of(H.p_kt, left);
-      seg = kv * H.p_rt + r;
+    if (w) {
+      row = (t - head[1].t0) * a.group + sub;
+      r = few ? row / FewCut::kRows : row / ManyCut::kRows;
+      left = head[1].p_rows - r * tile;
+      ua = kv * head[1].p_head + r * extent_of(head[1].p_kt, tile);
+      ext = extent_of(head[1].p_kt, left);
+      seg = kv * head[1].p_rt + r;
     } else {
-      const SeqPlan s = S.seqs[seq];
       const int rows = s.count * a.group;
       row = (t - s.first) * a.group + sub;
-      r = row / (unsigned)tile;
+      r = few ? row / FewCut::kRows : row / ManyCut::kRows;
       left = rows - r * tile;
       auto own = [&](int i) {
-        return extent_of(S.few ? own_tiles<FewCut>(a.by_group, rows, s.len, s.before, i)
-                               : own_tiles<ManyCut>(a.by_group, rows, s.len, s.before, i), rows - i * tile);
+        return extent_of(few ? own_tiles<FewCut>(a.by_group, rows, s.len, s.before, i)
+                             : own_tiles<ManyCut>(a.by_group, rows, s.len, s.before, i), rows - i * tile);
       };
       int before = 0;   // units of the head's row tiles before this one
       if (r > 0) {
@@ -1320,42 +1329,60 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
       }
       ua = s.units_before + kv * s.head + before;
       ext = own(r);
-      seg = s.segs_before + kv * ((rows + tile - 1) / (unsigned)tile) + r;
+      seg = s.segs_before + kv * (few ? up_div(rows, FewCut::kRows) : up_div(rows, ManyCut::kRows)) + r;
     }
     if (ext == 0) continue;
-    // its partials: few rows one a block; many rows the way of the row's half of a wide tile, or two
     row -= r * tile;
-    const int c0 = (unsigned)ua / (unsigned)H.width, c1 = (unsigned)(ua + ext - 1) / (unsigned)H.width;
-    int x = seg + c0, end = seg + c1 + 1, step = 1;
-    if (!S.few) {
-      x *= 2;
-      end *= 2;
+    const unsigned width = (unsigned)head[w].width;
+    const int c0 = (unsigned)ua / width, c1 = (unsigned)(ua + ext - 1) / width;
+    // few rows: one partial a block; many: the way of the row's half of a wide tile, or both ways
+    first[w] = seg + c0;
+    count[w] = c1 - c0 + 1;
+    if (!few) {
+      first[w] *= 2;
       if (left > 128) {
-        x += row >> 7;
+        first[w] += row >> 7;
         row &= 127;
-        step = 2;
+        step[w] = 2;
+      } else {
+        count[w] *= 2;
       }
     }
-    end = min(end, S.n_partials);
-#pragma unroll 2
-    for (; x < end; x += step) {
-      const long long at = (long long)x * S.rows_alloc + row;
-      const float2 p = S.ml[at];
-      if (p.x == -INFINITY) continue;   // nothing seen; its output row need not have been written
-      float v[E];
-      if constexpr (E == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(S.part + at * D + lane * 4);
-        v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(S.part + at * D + lane * 2);
-        v[0] = y.x, v[1] = y.y;
-      }
-      const float now = fmaxf(m, p.x);
-      const float f0 = exp2_fast(m - now), f1 = exp2_fast(p.x - now);
-      m = now;
-      l = l * f0 + p.y * f1;
+    at[w] = row;
+  }
+  float acc[E] = {}, m = -INFINITY, l = 0.f;
+  const int total = count[0] + count[1];
+#pragma unroll 1
+  for (int i0 = 0; i0 < total; i0 += 4) {
+    float2 p[4];
+    float v[4][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
+    for (int i = 0; i < 4; ++i) {
+      const int k = i0 + i, w = k >= count[0];
+      const int x = first[w] + (k - (w ? count[0] : 0)) * step[w];
+      p[i] = make_float2(-INFINITY, 0.f);
+      if (k < total && x < a.set[w].n_partials) {
+        const long long y = (long long)x * a.set[w].rows_alloc + at[w];
+        p[i] = a.set[w].ml[y];
+        const float* src = a.set[w].part + y * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 z = *reinterpret_cast<const float4*>(src);
+          v[i][0] = z.x, v[i][1] = z.y, v[i][2] = z.z, v[i][3] = z.w;
+        } else {
+          const float2 z = *reinterpret_cast<const float2*>(src);
+          v[i][0] = z.x, v[i][1] = z.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p[i].x == -INFINITY) continue;   // nothing seen; what stands in its row need not have been written
+      const float now = fmaxf(m, p[i].x);
+      const float f0 = exp2_fast(m - now), f1 = exp2_fast(p[i].x - now);
+      m = now;
+      l = l * f0 + p[i].y * f1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + v[i][e] * f1;
     }
   }
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
