@@ -40,7 +40,7 @@ struct FewCut {
   static constexpr int kRows = 16, kKeys = 64, kSetup = 1;
 };
 struct ManyCut {
-  static constexpr int kRows = 256, kKeys = 128, kSetup = 4;
+  static constexpr int kRows = 256, kKeys = 128, kSetup = 5;
 };
 constexpr int kMaxUnits = 0x7fffffff;
 
@@ -709,8 +709,8 @@ done:
 constexpr int kTile = 128;          // rows of a group's query tile
 constexpr int kKeys = ManyCut::kKeys;
 constexpr int kManyThreads = 384;   // two softmax groups, and one whose first three warps load and multiply
-// The launch's registers, 168 a thread, are shared out again: 2 x 208 + 88 = 3 x 168.
-constexpr int kSoftmaxRegs = 208, kIssueRegs = 88;
+// The launch's registers, 168 a thread, are shared out again: 2 x 224 + 56 = 3 x 168.
+constexpr int kSoftmaxRegs = 224, kIssueRegs = 56;
 template <int D> constexpr int kQueryBytes = kTile * D * 2;
 template <int D> constexpr int kKeyBytes = kKeys * D * 2;
 // K and V tiles in flight (a K tile is done with half a step earlier).
@@ -736,17 +736,6 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
       "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(shared_addr(b)), "r"(parity), "r"(1000u)
-      : "memory");
-  return ok != 0;
-}
-// Have both phases ended?
-__device__ __forceinline__ bool mbar_try2(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %5;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4, %5;\n\tand.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(shared_addr(x)), "r"(px), "r"(shared_addr(y)), "r"(py), "r"(1000u)
       : "memory");
   return ok != 0;
 }
@@ -906,15 +895,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   unsigned char* const ks = smem + 2 * QB;   // [RK] K tiles
   unsigned char* const vs = ks + RK * KB;    // [RV] V tiles
   // k_full, v_full: a ring slot holds its tile; k_free: it has been read (both groups say so, or one twice), v_free:
-  // likewise; q_full: a group's queries are in place; s_full: its scores are complete; p_full: the first, second half
-  // of its weights are in place; o_full: a piece's last PV is done.
+  // likewise; s_full: a group's scores are complete; o_full: a piece's last PV is done.
   // A parity tells whether a phase has ended only to one who knows that the phase before it has.  Within a group that
   // follows from the order of its steps.  A ring slot's last tile may have been the other group's: `loads` counts the
   // tiles whose loads have begun, and one begins only when the slot's last tile has landed and been read.
   __shared__ __align__(8) uint64_t k_full[RK], k_free[RK], v_full[RV], v_free[RV];
-  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[4], o_full[2];
+  __shared__ __align__(8) uint64_t s_full[2], o_full[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile uint32_t loads;
+  __shared__ volatile uint32_t loads[2];   // of K, of V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   lb::dependent_begin();
@@ -926,7 +914,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 0) {
-    loads = 0;
+    loads[0] = loads[1] = 0;
     for (int i = 0; i < RK; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_free[i], 2);
@@ -936,10 +924,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&v_free[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], 4);
-      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -960,7 +945,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // ---- loads: lane i brings the i-th page of a tile
       const int box = min(1 << a.page_shift, kKeys);   // rows of a copy
       auto load = [&](const CUtensorMap* map, unsigned char* slot, uint64_t* full, int key, int boxes, int page) {
-        if (lane == 0) mbar_expect(full, boxes * box * D * 2);
+        if (lane == 0) {
+          mbar_expect(full, boxes * box * D * 2);
+          __threadfence_block();   // before `loads` says so
+        }
         __syncwarp();
         if (lane < boxes) {
 #pragma unroll
@@ -985,85 +973,19 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             }
           }
           if (n >= RK) wait(&k_free[n % RK], (n / RK - 1) & 1);
-          if (n >= RV) wait(&v_free[n % RV], (n / RV - 1) & 1);
           if (dead) break;
           load(&map_k, ks + n % RK * KB, &k_full[n % RK], key, boxes, page);
+          if (lane == 0) loads[0] = n + 1;
+          if (n >= RV) wait(&v_free[n % RV], (n / RV - 1) & 1);
+          if (dead) break;
           load(&map_v, vs + n % RV * KB, &v_full[n % RV], key, boxes, page);
-          if (lane == 0) {
-            __threadfence_block();
-            loads = n + 1;
-          }
+          if (lane == 0) loads[1] = n + 1;
         }
       } while (!dead && pc.next(a));
       if (dead && lane == 0) {   // copies under way land before the block ends
         for (uint32_t x = n > RK ? n - RK : 0; x < n; ++x) mbar_wait(&k_full[x % RK], (x / RK) & 1);
         for (uint32_t x = n > RV ? n - RV : 0; x < n; ++x) mbar_wait(&v_full[x % RV], (x / RV) & 1);
       }
-    } else if (warp < 11) {
-      // ---- products of group g.  The whole warp walks, one elected lane issues: control flow and operands that are
-      // uniform for the warp let descriptors live in uniform registers (with lane 0 alone in a branch, moving them
-      // there took 65 cycles a product, more than the tensor core needs for it).  One warp for both groups was not
-      // enough: a product's waits, issue and commit take it some 500 cycles.
-      const int g = warp - 9;
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + 128 * g;   // S, P, P; O 256 columns on
-      constexpr uint32_t pv = mma_shape<T>(kTile, D, true);
-      // a negative scale negates the queries, so that the softmax knows positive ones only
-      const uint32_t qk = mma_shape<T>(kTile, kKeys, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
-      const uint64_t q = tile_desc(shared_addr(qs) + g * QB, 16, 1024);
-      uint32_t s = 0, pieces = 0;       // steps, pieces with steps before
-      uint32_t begun = 0;               // loads, as last seen
-      // both barriers at once: their latencies are most of what a step costs this warp
-      auto wait = [&](uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) {
-        for (int spin = 0; !dead && !mbar_try2(x, px, y, py); ++spin) dead = spin > lb::kSpinLimit;
-      };
-      do {
-        const bool wide = __shfl_sync(0xffffffffu, (int)(pc.rows_left() > kTile), 0);
-        const int tiles = __shfl_sync(0xffffffffu, pc.t1 - pc.t0, 0);
-        const int total = wide ? tiles : (tiles - g + 1) / 2;
-        const uint32_t inc = wide ? 1 : 2;
-        uint32_t x = n + (wide ? 0 : g);   // the step's tile
-        uint32_t vslot = x % RV, vphase = (x / RV) & 1;
-        for (int i = 0; i < total; ++i, ++s, x += inc) {
-          for (int spin = 0; begun <= x && !dead; ++spin) {
-            begun = __shfl_sync(0xffffffffu, loads, 0);
-            dead = spin > lb::kSpinLimit;
-          }
-          wait(&k_full[x % RK], (x / RK) & 1, &q_full[g], pieces & 1);
-          tc_after();
-          const uint64_t k = tile_desc(shared_addr(ks) + x % RK * KB, 16, 1024);
-          if (elect_one()) {
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-              mma_ss(tm, q + ((c >> 2) * QHALF + (c & 3) * 32) / 16, k + ((c >> 2) * KHALF + (c & 3) * 32) / 16, qk, c > 0);
-            tc_commit(&s_full[g]);
-          }
-          __syncwarp();
-          const uint64_t v = tile_desc(shared_addr(vs) + vslot * KB, KHALF, 1024);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            wait(&v_full[vslot], vphase, &p_full[2 * g + half], s & 1);
-            tc_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int c = 4 * half; c < 4 * half + 4; ++c)
-                mma_ts(tm + 256, tm + 8 * c, v + c * 2048 / 16, pv, i > 0 || c > 0);
-              if (half) {
-                tc_commit(&v_free[vslot]);
-                if (!wide) mbar_arrive(&v_free[vslot]);
-                if (i + 1 == total) tc_commit(&o_full[g]);
-              }
-            }
-            __syncwarp();
-          }
-          vslot += inc;
-          if (vslot >= RV) {
-            vslot -= RV;
-            vphase ^= 1;
-          }
-        }
-        pieces += total > 0;
-        n += tiles;
-      } while (!dead && pc.next(a));
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -1074,6 +996,51 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + 128 * g + lane0, to = tmem + 256 + 128 * g + lane0;
     const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);   // above 0, so that -inf stays -inf
+    // The group's first warp issues its products, one elected lane of it; what is uniform for the warp (tm, gg) is
+    // made so for the compiler, so that the descriptors live in uniform registers.
+    const bool issuer = (warp & 3) == 0;
+    const uint32_t gg = __shfl_sync(0xffffffffu, (uint32_t)g, 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + 128 * gg;   // S and P; O 256 columns on
+    constexpr uint32_t pv = mma_shape<T>(kTile, D, true);
+    // a negative scale negates the queries, so that the softmax knows positive ones only
+    const uint32_t qk = mma_shape<T>(kTile, kKeys, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+    const uint64_t q_desc = tile_desc(shared_addr(qs) + gg * QB, 16, 1024);
+    uint32_t begun[2] = {0, 0};   // loads, as last seen
+    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
+    // tile x of K (0) or V (1) is there
+    auto landed = [&](int kv, uint32_t x, uint64_t* full, uint32_t parity) {
+      for (int spin = 0; begun[kv] <= x && !dead; ++spin) {
+        begun[kv] = __shfl_sync(0xffffffffu, loads[kv], 0);
+        dead = spin > lb::kSpinLimit;
+      }
+      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(full, parity));
+      tc_after();
+    };
+    // tile x: S = Q K^T
+    auto score = [&](uint32_t x) {
+      landed(0, x, &k_full[x % RK], (x / RK) & 1);
+      const uint64_t k = tile_desc(shared_addr(ks) + x % RK * KB, 16, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          mma_ss(tm, q_desc + ((c >> 2) * QHALF + (c & 3) * 32) / 16, k + ((c >> 2) * KHALF + (c & 3) * 32) / 16, qk, c > 0);
+        tc_commit(&s_full[gg]);
+      }
+      __syncwarp();
+    };
+    // tile x: O (+)= P V; `once`: nobody else reads the tile
+    auto weigh = [&](uint32_t x, bool add, bool once, bool last) {
+      landed(1, x, &v_full[x % RV], (x / RV) & 1);
+      const uint64_t v = tile_desc(shared_addr(vs) + x % RV * KB, KHALF, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < kKeys / 16; ++c) mma_ts(tm + 256, tm + 8 * c, v + c * 2048 / 16, pv, add || c > 0);
+        tc_commit(&v_free[x % RV]);
+        if (once) mbar_arrive(&v_free[x % RV]);
+        if (last) tc_commit(&o_full[gg]);
+      }
+      __syncwarp();
+    };
     uint32_t steps = 0, pieces = 0;
     auto steps_of = [&](const Piece<ManyCut>& x) {   // of this group
       const int tiles = x.t1 - x.t0;
@@ -1108,8 +1075,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (mine > 0) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         async_fence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[g]);
+        group_sync();
+        if (issuer) score(n + (wide ? 0 : g));
         for (int j = 0; j < mine; ++j, ++steps) {
           const int tile = wide ? j : 2 * j + g;
           const int key = (pc.t0 + tile) * kKeys;
@@ -1157,7 +1124,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
           if (pc.len - key < kKeys) {   // V rows past the end (both groups of a wide segment write the same zeros)
             const uint32_t x = n + tile;
-            if (!dead && !mbar_wait(&v_full[x % RV], (x / RV) & 1)) dead = true;
+            landed(1, x, &v_full[x % RV], (x / RV) & 1);
             if (row >= pc.len - key) {
 #pragma unroll
               for (int c = 0; c < D / 8; ++c)
@@ -1165,7 +1132,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                     make_uint4(0, 0, 0, 0);
             }
             async_fence();
-            dead = __any_sync(0xffffffffu, dead);
           }
           const float base = m == -INFINITY ? 0.f : m;
           const uint64_t scale2 = pair(scale, scale), base2 = pair(-base, -base);
@@ -1193,10 +1159,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               }
             }
             tmem_store32(ts + 32 * half, s + 32 * half);
-            tmem_store_wait();
-            tc_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * g + half]);
+          }
+          tmem_store_wait();
+          tc_before();
+          group_sync();
+          if (issuer) {
+            weigh(n + tile, j > 0, !wide, j + 1 == mine);
+            if (j + 1 < mine) score(n + tile + (wide ? 1 : 2));
           }
           const float2 sum = split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
           l += sum.x + sum.y;
@@ -1230,7 +1199,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
       n += tiles;
       pc = nx;
-    } while (!dead && more);
+    } while (more);   // all warps of a group walk on together, dead or not: they meet at its barrier
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   if (dead) bad |= lb::kStatusTimeout;
