@@ -40,7 +40,7 @@ struct FewCut {
   static constexpr int kRows = 16, kKeys = 64, kSetup = 1;
 };
 struct ManyCut {
-  static constexpr int kRows = 256, kKeys = 128, kSetup = 5;
+  static constexpr int kRows = 256, kKeys = 128, kSetup = 9;
 };
 constexpr int kMaxUnits = 0x7fffffff;
 
@@ -873,6 +873,12 @@ __device__ __forceinline__ float2 exp2_poly(uint64_t x) {
                      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 bytes at once, a whole sector: lanes write rows far apart
+__device__ __forceinline__ void store32(float* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tma_page(void* dst, const CUtensorMap* map, int x, int row, int head, int page,
                                          uint64_t* bar) {
@@ -905,6 +911,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __shared__ volatile uint32_t loads[2];   // of K, of V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (threadIdx.x < 2)   // the maps are kernel arguments: they can be fetched before the work before this is done
+    asm volatile("prefetch.tensormap [%0];" ::"l"(threadIdx.x ? &map_v : &map_k) : "memory");
   lb::dependent_begin();
   const Begin b = plan_block<ManyCut, kManyThreads>(a);
   if (b.u0 >= b.u1) return;   // the whole block
@@ -1028,16 +1036,20 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
       __syncwarp();
     };
-    // tile x: O (+)= P V; `once`: nobody else reads the tile
-    auto weigh = [&](uint32_t x, bool add, bool once, bool last) {
-      landed(1, x, &v_full[x % RV], (x / RV) & 1);
+    // tile x, half of its keys: O (+)= P V; `once`: nobody else reads the tile
+    auto weigh = [&](uint32_t x, bool add, bool once, bool last, int half) {
+      if (!half) landed(1, x, &v_full[x % RV], (x / RV) & 1);
+      else tc_after();
       const uint64_t v = tile_desc(shared_addr(vs) + x % RV * KB, KHALF, 1024);
       if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < kKeys / 16; ++c) mma_ts(tm + 256, tm + 8 * c, v + c * 2048 / 16, pv, add || c > 0);
-        tc_commit(&v_free[x % RV]);
-        if (once) mbar_arrive(&v_free[x % RV]);
-        if (last) tc_commit(&o_full[gg]);
+        for (int c = 0; c < kKeys / 32; ++c)
+          mma_ts(tm + 256, tm + 8 * (c + 4 * half), v + (c + 4 * half) * 2048 / 16, pv, add || c + half > 0);
+        if (half) {
+          tc_commit(&v_free[x % RV]);
+          if (once) mbar_arrive(&v_free[x % RV]);
+          if (last) tc_commit(&o_full[gg]);
+        }
       }
       __syncwarp();
     };
@@ -1083,13 +1095,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (!dead && !mbar_wait(&s_full[g], steps & 1)) dead = true;
           dead = __any_sync(0xffffffffu, dead);
           tc_after();
+          uint32_t s[kKeys];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_load32(ts + 32 * c, s + 32 * c);
           if ((threadIdx.x & 127) == 0) {   // the products that made these scores have read the K tile
             mbar_arrive(&k_free[(n + tile) % RK]);
             if (!wide) mbar_arrive(&k_free[(n + tile) % RK]);
           }
-          uint32_t s[kKeys];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_load32(ts + 32 * c, s + 32 * c);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_load_wait(s + 32 * c);
           if (__any_sync(0xffffffffu, key + kKeys > lim)) {
@@ -1159,13 +1171,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               }
             }
             tmem_store32(ts + 32 * half, s + 32 * half);
-          }
-          tmem_store_wait();
-          tc_before();
-          group_sync();
-          if (issuer) {
-            weigh(n + tile, j > 0, !wide, j + 1 == mine);
-            if (j + 1 < mine) score(n + tile + (wide ? 1 : 2));
+            tmem_store_wait();
+            tc_before();
+            group_sync();
+            if (issuer) {
+              weigh(n + tile, j > 0, !wide, j + 1 == mine, half);
+              if (half && j + 1 < mine) score(n + tile + (wide ? 1 : 2));
+            }
           }
           const float2 sum = split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
           l += sum.x + sum.y;
@@ -1192,8 +1204,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           tmem_load_wait(o);
           if (keep)
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 32; i += 8) store32(dst + 32 * c + i, o + i);
         }
         tc_before();
       }
@@ -1234,7 +1245,7 @@ struct JoinArgs {
 
 // One warp per (token, query head): finds the token's sequence, weighs the
 // row's partials of both key sets and writes the output.  Bound by latency at
-// decode sizes: the plan is one round of loads, the first four partials another.
+// decode sizes: the plan is one round of loads, the first eight partials another.
 template <class T, int D>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int E = D / 32;
@@ -1321,12 +1332,13 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   }
   float acc[E] = {}, m = -INFINITY, l = 0.f;
   const int total = count[0] + count[1];
+  constexpr int kAtOnce = 8;
 #pragma unroll 1
-  for (int i0 = 0; i0 < total; i0 += 4) {
-    float2 p[4];
-    float v[4][E];
+  for (int i0 = 0; i0 < total; i0 += kAtOnce) {
+    float2 p[kAtOnce];
+    float v[kAtOnce][E];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAtOnce; ++i) {
       const int k = i0 + i, w = k >= count[0];
       const int x = first[w] + (k - (w ? count[0] : 0)) * step[w];
       p[i] = make_float2(-INFINITY, 0.f);
@@ -1344,7 +1356,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAtOnce; ++i) {
       if (p[i].x == -INFINITY) continue;   // nothing seen; what stands in its row need not have been written
       const float now = fmaxf(m, p[i].x);
       const float f0 = exp2_fast(m - now), f1 = exp2_fast(p[i].x - now);
