@@ -44,11 +44,7 @@ struct ManyCut {
 };
 constexpr int kMaxUnits = 0x7fffffff;
 
-// Division by a number fixed at launch, exact for 0 <= n < 2^31.
-struct Divisor {
-  unsigned mul, shift;
-  __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi(mul, (unsigned)n) + (unsigned)n) >> shift); }
-};
+using lb::Divisor;
 
 // A plane of one cache, strides in bytes.
 struct PlaneArg {
@@ -1388,13 +1384,6 @@ int sm_count() {
   return e || v < 1 ? 148 : v;
 }
 
-Divisor divisor(int d) {
-  Divisor r{0, 0};
-  while ((1u << r.shift) < (unsigned)d) ++r.shift;
-  r.mul = (unsigned)((((uint64_t)1 << 32) * (((uint64_t)1 << r.shift) - d)) / d + 1);
-  return r;
-}
-
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 // Work memory of one launch: [head][sequences][ml][partials].
@@ -1582,7 +1571,7 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   a.most_q = most_q;
   a.heads = K.heads;
   a.group = group;
-  a.by_group = divisor(group);
+  a.by_group = lb::divisor(group);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = status;
   JoinArgs j{};

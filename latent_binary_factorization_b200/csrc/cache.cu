@@ -54,6 +54,7 @@ struct Side {
 struct RowJob {
   Side src, dst;
   int units;         // units of one row: a unit is 16 bytes, or the two 16-byte halves of eight pairs
+  lb::Divisor by_units;
   int rot_units;     // the first rot_units of them are rotated
   unsigned first;    // first item of the job within a token
 };
@@ -61,6 +62,7 @@ struct RowArgs {
   RowJob job[kMaxJobs];
   int n_jobs, n_tokens, per_block;   // per_block: tokens of one block
   unsigned items;                    // items of one token, over all jobs
+  lb::Divisor by_items, by_half;
   int page_shift;
   long long n_rows;                  // rows of the cache (bound of where)
   const long long* where;
@@ -91,10 +93,9 @@ __device__ __forceinline__ unsigned char* side_at(const Side& s, int t, long lon
                            : (long long)t * s.stride_major);
 }
 
-// What one item of the kernel is: where it reads and writes.
+// What one item of the kernel is.
 struct Item {
-  const unsigned char* src;
-  unsigned char* dst;
+  unsigned char* dst;      // null: nothing to do
   int unit, rot, second;   // second: bytes from the first chunk to the pair's second (0: one chunk)
   int token;               // within the block
 };
@@ -106,8 +107,11 @@ struct Item {
 //
 // A block takes per_block tokens.  Its threads first put cos and sin of the
 // tokens' pairs into shared memory (once for all heads of all tensors), with
-// the loads of their first item already under way; then each item is one or
-// two 16-byte loads, the rotation in fp32, and as many stores.
+// the loads of their first items already under way; then each item is one or
+// two 16-byte loads, the rotation in fp32, and as many stores.  One item a
+// thread at a time: eight blocks an SM hide the latency, and two or four items
+// a thread cost more in registers than they bring (a rotary prompt of 2048
+// tokens x 72 heads, bf16: 18.4 us with one, 19.8 with two, 33 with four).
 template <class T>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowArgs a) {
   constexpr int E = 16 / sizeof(T);
@@ -115,19 +119,22 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowAr
   lb::dependent_begin();
   const int t0 = blockIdx.x * a.per_block;
   const int n_tok = min(a.per_block, a.n_tokens - t0);
-  const unsigned total = a.items * (unsigned)n_tok;
-  const unsigned step = gridDim.y * blockDim.x;
-  unsigned it = blockIdx.y * blockDim.x + threadIdx.x;
+  const int total = (int)a.items * n_tok, step = gridDim.y * blockDim.x;
 
-  auto locate = [&](unsigned i, Item& o) -> bool {
-    o.token = (int)(i / a.items);
-    const unsigned r = i - (unsigned)o.token * a.items;
+  Item o;
+  Chunk<T> x, y;
+  // item i of the block: where it is, and its loads
+  auto begin = [&](int i) {
+    o.dst = nullptr;
+    if (i >= total) return;
+    o.token = a.per_block > 1 ? a.by_items(i) : 0;
+    const int r = i - o.token * (int)a.items;
     int j = 0;
-    while (j + 1 < a.n_jobs && r >= a.job[j + 1].first) ++j;
+    while (j + 1 < a.n_jobs && r >= (int)a.job[j + 1].first) ++j;
     const RowJob& J = a.job[j];
-    const unsigned k = r - J.first;
-    const int head = (int)(k / (unsigned)J.units);
-    o.unit = (int)(k - (unsigned)head * J.units);
+    const int k = r - (int)J.first;
+    const int head = J.by_units(k);
+    o.unit = k - head * J.units;
     o.rot = o.unit < J.rot_units;
     // half layout: rotated units hold two chunks half a rotary width apart
     const int halves = J.rot_units > 0 && !a.interleaved;
@@ -137,27 +144,48 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowAr
     long long w = 0;
     if (J.src.paged || J.dst.paged) {
       w = a.where[t];
-      if (w < 0) return false;
+      if (w < 0) return;
       if (w >= a.n_rows) {
         atomicOr(&g_status, kStatusIndex);
-        return false;
+        return;
       }
     }
-    o.src = side_at(J.src, t, w, a.page_shift) + (long long)head * J.src.stride_head + 16 * chunk;
+    const unsigned char* src = side_at(J.src, t, w, a.page_shift) + (long long)head * J.src.stride_head + 16 * chunk;
     o.dst = side_at(J.dst, t, w, a.page_shift) + (long long)head * J.dst.stride_head + 16 * chunk;
-    return true;
+    x.u = *reinterpret_cast<const uint4*>(src);
+    if (o.second) y.u = *reinterpret_cast<const uint4*>(src + o.second);
+  };
+  auto finish = [&]() {
+    if (!o.dst) return;
+    if (o.rot) {
+      const float2* cs = turn + o.token * a.half;
+      if (a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 w = cs[(o.unit * E + e) >> 1];
+          const float p = to_f(x.e[e]), q = to_f(x.e[e + 1]);
+          x.e[e] = from_f<T>(p * w.x - q * w.y);
+          x.e[e + 1] = from_f<T>(q * w.x + p * w.y);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float2 w = cs[o.unit * E + e];
+          const float p = to_f(x.e[e]), q = to_f(y.e[e]);
+          x.e[e] = from_f<T>(p * w.x - q * w.y);
+          y.e[e] = from_f<T>(q * w.x + p * w.y);
+        }
+      }
+    }
+    *reinterpret_cast<uint4*>(o.dst) = x.u;
+    if (o.second) *reinterpret_cast<uint4*>(o.dst + o.second) = y.u;
   };
 
-  Item o;
-  Chunk<T> x, y;
-  bool have = it < total && locate(it, o);
-  if (have) {
-    x.u = *reinterpret_cast<const uint4*>(o.src);
-    if (o.second) y.u = *reinterpret_cast<const uint4*>(o.src + o.second);
-  }
+  int it = blockIdx.y * blockDim.x + threadIdx.x;
+  begin(it);
   if (a.half) {
     for (int i = threadIdx.x; i < n_tok * a.half; i += blockDim.x) {
-      const int t = i / a.half;
+      const int t = a.by_half(i);
       // signed fraction of a turn in 64 bits; times 2^-63: the argument of sincospi
       const long long f = (long long)((uint64_t)(long long)a.positions[t0 + t] * a.phases[i - t * a.half]);
       float s, c;
@@ -166,37 +194,9 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowAr
     }
     __syncthreads();
   }
-  while (it < total) {
-    if (have) {
-      if (o.rot) {
-        const float2* cs = turn + o.token * a.half;
-        if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float2 w = cs[(o.unit * E + e) >> 1];
-            const float p = to_f(x.e[e]), q = to_f(x.e[e + 1]);
-            x.e[e] = from_f<T>(p * w.x - q * w.y);
-            x.e[e + 1] = from_f<T>(q * w.x + p * w.y);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float2 w = cs[o.unit * E + e];
-            const float p = to_f(x.e[e]), q = to_f(y.e[e]);
-            x.e[e] = from_f<T>(p * w.x - q * w.y);
-            y.e[e] = from_f<T>(q * w.x + p * w.y);
-          }
-        }
-      }
-      *reinterpret_cast<uint4*>(o.dst) = x.u;
-      if (o.second) *reinterpret_cast<uint4*>(o.dst + o.second) = y.u;
-    }
+  for (; it < total; begin(it)) {
+    finish();
     it += step;
-    have = it < total && locate(it, o);
-    if (have) {
-      x.u = *reinterpret_cast<const uint4*>(o.src);
-      if (o.second) y.u = *reinterpret_cast<const uint4*>(o.src + o.second);
-    }
   }
 }
 
@@ -792,9 +792,9 @@ cudaError_t allow_smem(K kern, lb::PerDevice& slot, int bytes) {
 template <class T>
 lb_status launch_rows_of(const RowArgs& a, cudaStream_t st) {
   const int x = lb::ceil_div(a.n_tokens, a.per_block);
-  // blocks that share a token's items: enough for four blocks an SM, none without work
+  // blocks that share a group's items: four blocks an SM, four a group at least, none without work
   const int64_t need = ((int64_t)a.items * a.per_block + 255) / 256;
-  const int y = (int)std::min<int64_t>(std::min<int64_t>(need, 1024), std::max(1, 148 * 4 / x));
+  const int y = (int)std::min<int64_t>(std::min<int64_t>(need, 1024), std::max(a.per_block, 148 * 4 / x));
   return launched(lb::launch_dependent_on(st, rows_kernel<T>, dim3(x, y), 256,
                                           (size_t)a.per_block * a.half * sizeof(float2), a));
 }
@@ -822,6 +822,7 @@ struct RowLaunch {
     J.dst = dst;
     J.rot_units = rotary_dim / (a.interleaved ? 1 : 2) / E;
     J.units = J.rot_units + (width - rotary_dim) / E;
+    J.by_units = lb::divisor(J.units);
     J.first = a.items;
     a.items += (unsigned)heads * (unsigned)J.units;
   }
@@ -839,8 +840,10 @@ struct RowLaunch {
     a.where = reinterpret_cast<const long long*>(where);
   }
   lb_status launch(cudaStream_t st) {
-    // four tokens a block share its set-up when there are tokens enough to fill the GPU so
-    a.per_block = a.n_tokens >= 4 * 148 * 4 ? 4 : 1;
+    // four tokens share a block's set-up when that leaves blocks enough (4096 tokens written: 30.9 us, 31.6 with one)
+    a.per_block = a.n_tokens >= 148 * 4 ? 4 : 1;
+    a.by_items = lb::divisor((int)a.items);
+    a.by_half = lb::divisor(std::max(a.half, 1));
     switch (dt) {
       case LB_F16: return launch_rows_of<__half>(a, st);
       case LB_BF16: return launch_rows_of<__nv_bfloat16>(a, st);

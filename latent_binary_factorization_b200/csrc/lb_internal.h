@@ -269,6 +269,23 @@ cudaError_t launch_dependent_on(cudaStream_t st, void (*kern)(P...), dim3 grid, 
 }
 #endif
 
+// Division by a number fixed at launch, exact for 0 <= n < 2^31: with 2^shift
+// >= d, (n mul / 2^32 + n) / 2^shift, mul = floor(2^32 (2^shift - d) / d) + 1.
+struct Divisor {
+  unsigned mul, shift;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi(mul, (unsigned)n) + (unsigned)n) >> shift);
+  }
+#endif
+};
+inline Divisor divisor(int d) {
+  Divisor r{0, 0};
+  while ((1u << r.shift) < (unsigned)d) ++r.shift;
+  r.mul = (unsigned)((((uint64_t)1 << 32) * (((uint64_t)1 << r.shift) - (unsigned)d)) / (unsigned)d + 1);
+  return r;
+}
+
 // cache.cu: argument checks shared with attend.cu, and the status word of the
 // paged cache's calls (null before the first of them on the device).
 lb_status check_cache(const lb_cache* c);
