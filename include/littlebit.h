@@ -359,7 +359,9 @@ lb_status littlebit_linear_forward_noalloc(const lb_layer* layer, const void* x_
  * of -1 in a list is padding and skipped.  Lists take up to 4096 entries.
  * Calls that change one cache must be ordered by the caller.  Alignment: every
  * plane's and row tensor's base on 16 bytes, strides and row sizes multiples
- * of 16 bytes.  None of these calls allocates device memory.
+ * of 16 bytes.  None of these calls allocates device memory or waits for the
+ * device; their kernels use programmatic dependent launch and begin with a wait
+ * for all work before them on the stream.
  */
 typedef struct lb_plane {
   void* data;
@@ -391,7 +393,7 @@ typedef struct lb_rows {
  *   (a, b) -> scale * (a cos - b sin, b cos + a sin),
  * with (a, b) at elements (i, i + rotary_dim/2), or (2i, 2i + 1) if
  * `interleaved`; elements from rotary_dim on are left alone.  inverse = 1
- * turns back (with scale 1 the transposed rotation, hence also the gradient).
+ * turns by the opposite angle: the transposed map, i.e. the gradient's.
  * phases holds f_i / 2 pi as 64-bit fractions of a turn, so that pos * phase
  * modulo 2^64 is the angle, without loss at any position.
  */
@@ -455,7 +457,8 @@ lb_status littlebit_cache_locate(const lb_cache* c, const int32_t* slots_dev, co
  * where -1 is skipped.  Planes whose bit i is set in `rotated` get the rows
  * rotated (rope, positions_dev).  q, if not null, is rotated into q_out by the
  * same launch (every token, also skipped ones).  All of one dtype, that of the
- * planes: LB_F16, LB_BF16 or LB_F32.  One launch.
+ * planes: LB_F16, LB_BF16 or LB_F32.  One launch.  Two tokens of one row leave
+ * either's values there.
  */
 lb_status littlebit_cache_write(const lb_cache* c, const int* planes, const lb_rows* rows, int n, int n_tokens,
                                 const int64_t* where_dev, const lb_rotary* rope, const int32_t* positions_dev,
@@ -521,6 +524,10 @@ lb_status littlebit_cache_copy(const lb_cache* c, const int32_t* src_dev, const 
  * sequence's end are never used, whatever they hold.  (A non-finite V of a
  * token may reach the outputs of earlier tokens of the same call and
  * sequence, whose weight for it is zero.)
+ * Two or three launches.  Limits: n_tokens * q.heads <= 2^22, max_pages *
+ * page_size <= 2^24 tokens; the planes' strides must be positive multiples of 16
+ * bytes below 2^40.  A page number outside the cache counts as a page of zeros
+ * and raises LB_ERR_INDEX; a slot outside it has no tokens and raises it too.
  * work_dev: littlebit_cache_attend_work bytes, 256-byte aligned, needed until
  * the call's launches are done; calls that may overlap need their own.
  * Errors: LB_ERR_ARG, LB_ERR_SHAPE, LB_ERR_ALIGN, LB_ERR_UNSUPPORTED (dtype
@@ -546,7 +553,8 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
  * The word of littlebit_linear_forward_noalloc on the current device is read
  * and cleared too (its calls may be on any stream: synchronise them first), and
  * likewise the word of the paged cache's calls on the current device, whose
- * bits are (1 << LB_ERR_PAGES) and (1 << LB_ERR_INDEX) (see there).
+ * bits are (1 << LB_ERR_PAGES), (1 << LB_ERR_INDEX) and, from its attention,
+ * (1 << LB_ERR_TIMEOUT) (see there).
  * *status is 0 when nothing was raised.  Errors: LB_ERR_ARG, LB_ERR_CUDA.
  */
 lb_status littlebit_device_status(void* stream, unsigned int* status);

@@ -76,7 +76,8 @@ def rotate(xs: list, positions: torch.Tensor, rope: Rotary, outs: list | None = 
            stream=None) -> list:
     """Rotated rows of up to eight tensors (tokens, heads, width), fp16, bf16 or
     fp32, one dtype, in one launch.  ``outs`` may be ``xs`` (in place).
-    inverse turns back; with scale 1 that is also the gradient of the rotation."""
+    inverse turns back; with any scale it is also the transpose, i.e. the
+    gradient of the rotation (autograd does not see these calls)."""
     if stream is not None:
         with _on(stream, rope.device):
             return _b.rotate(rope._h, xs, positions, outs, inverse)
@@ -93,7 +94,7 @@ class Cache:
 
     def __init__(self, planes: list, table: torch.Tensor, length: torch.Tensor, refs: torch.Tensor):
         self._h = _b.cache(planes, table, length, refs)
-        self.planes, self.table, self.length, self.refs = list(planes), table, length, refs
+        self._tensors = tuple(planes), table, length, refs   # the handle holds their addresses
         self.device = table.device
         self.n_pages, self.page_size = planes[0].shape[0], planes[0].shape[2]
         self.n_slots, self.max_pages = table.shape
@@ -106,6 +107,12 @@ class Cache:
         return cls(planes, torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros(n_slots, dtype=torch.int32, device=device),
                    torch.zeros(n_pages, dtype=torch.int32, device=device))
+
+    # the cache's tensors; to go on with others (as compact(into=True) gives), make another Cache
+    planes = property(lambda self: self._tensors[0])
+    table = property(lambda self: self._tensors[1])
+    length = property(lambda self: self._tensors[2])
+    refs = property(lambda self: self._tensors[3])
 
     # ---- bookkeeping
     def extend(self, slots: torch.Tensor, starts: torch.Tensor, tokens: int, prefix: int = -1, out=None, stream=None):
@@ -146,15 +153,11 @@ class Cache:
         """Moves the pages in use to the lowest numbers.  Returns (table, refs,
         count of pages in use): the cache's own tensors, updated, or with
         ``into`` new ones, the cache's staying as they are (and the rows they
-        lead to good until a page is taken)."""
+        lead to good until a page is taken); go on with a Cache of the new."""
         if stream is not None:
             with _on(stream, self.device):
-                return self.compact(into)
-        table, refs = self.table, self.refs
-        if into:
-            table, refs = torch.empty_strided(table.shape, table.stride(), dtype=torch.int32,
-                                              device=self.device), torch.empty_like(refs)
-        return table, refs, _b.compact(self._h, table, refs)
+                return _b.compact(self._h, self.table, self.refs, into)
+        return _b.compact(self._h, self.table, self.refs, into)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copies page src[i] to page dst[i] in every plane."""

@@ -35,12 +35,15 @@ constexpr unsigned kStatusIndex = 1u << LB_ERR_INDEX;
 
 // How a kernel cuts its segments: query rows of a tile, keys of a tile, units
 // that a segment's beginning and end are worth, units of one key tile.  A wide
-// row tile, of more than 128 rows, costs two (see many_rows_kernel).
+// row tile, of more than 128 rows, costs two (see many_rows_kernel).  kSetup is
+// measured: with 3, 5, 6, 9 and 12 a batch of pieces of prompts (16 sequences of
+// up to 130 tokens over a prefix of 12000, each with own keys) took 727, 560,
+// 551, 557 and 566 us, as its short segments end late or early.
 struct FewCut {
   static constexpr int kRows = 16, kKeys = 64, kSetup = 1;
 };
 struct ManyCut {
-  static constexpr int kRows = 256, kKeys = 128, kSetup = 9;
+  static constexpr int kRows = 256, kKeys = 128, kSetup = 6;
 };
 constexpr int kMaxUnits = 0x7fffffff;
 
@@ -97,6 +100,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The larger of two, NaN if one is: a NaN score makes its row NaN, as a sum over it would be.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t shared_addr(const void* p) {
@@ -253,6 +263,11 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
   if (b.u0 < p_units || b.u0 >= b.u1) return b;
   u = p_units;
   segs = p_segs;
+  if (n > THREADS && tid == 0) {   // lengths that changed since the first sweep may leave u0 without a place
+    found[0] = 0;
+    found[1] = b.u0;
+    found[2] = p_segs;
+  }
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += THREADS) {
     if (n > THREADS) step(i0, false);
@@ -565,14 +580,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
         for (int e = 0; e < 4; ++e) {
           const int at = key + 8 * n + 2 * c + (e & 1);
           s[n][e] = at < lim[e >> 1] ? s[n][e] * a.scale_log2 : -INFINITY;
-          top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+          top[e >> 1] = max_nan(top[e >> 1], s[n][e]);
         }
       float alpha[2], base[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-        const float now = fmaxf(m[i], top[i]);
+        top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+        top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+        const float now = max_nan(m[i], top[i]);
         base[i] = now == -INFINITY ? 0.f : now;
         alpha[i] = exp2_fast(m[i] - base[i]);
         m[i] = now;
@@ -622,13 +637,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
     for (int i = 0; i < 2; ++i) {
       float top = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) top = fmaxf(top, stat[x][g + 8 * i].x);
+      for (int x = 0; x < 4; ++x) top = max_nan(top, stat[x][g + 8 * i].x);
       f[i] = top == -INFINITY ? 0.f : exp2_fast(m[i] - top);
     }
     if (threadIdx.x < rows) {
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) top = fmaxf(top, stat[x][threadIdx.x].x);
+      for (int x = 0; x < 4; ++x) top = max_nan(top, stat[x][threadIdx.x].x);
       if (top != -INFINITY)
 #pragma unroll
         for (int x = 0; x < 4; ++x) sum += exp2_fast(stat[x][threadIdx.x].x - top) * stat[x][threadIdx.x].y;
@@ -677,7 +692,7 @@ done:
 //
 // A block has two softmax groups of four warps, each with a tile of 128 query
 // rows in shared memory.  One warp loads K and V tiles of 128 keys by TMA, page
-// by page, into rings; two warps issue the products of a group each:
+// by page, into rings.  The products are
 //   S = Q K^T (both from shared memory), O += P V (P from tensor memory, V as
 //   it lies, keys down, i.e. N-major).
 // Each thread of a group owns one row, so the row's maximum and sum need no
@@ -691,12 +706,16 @@ done:
 // then hold P (16-bit pairs), and O (fp32, D columns): all 512 for D = 128.
 // A group is one chain, S(i) -> softmax -> PV(i) -> QK(i + 1), and while one is
 // in its softmax the other's products run; PV starts when half of P is there.
+// The group's first warp issues its products: a warp of their own had to be
+// woken for each, and took 700 us for 626.
 // The tensor core takes a group's products in order, so S(i + 1) being complete
 // means that PV(i) is, and no barrier guards P or O.  (Tiles of 64 keys with P
 // beside S, whose QK(i + 1) runs beside softmax i, have a shorter chain but fetch
-// Q twice as often, 192 bytes of shared memory a cycle where there are 128:
-// 4000 cycles for 256 rows x 128 keys against KCYC here; arithmetic alone takes
-// 2048.)
+// Q twice as often, 192 bytes of shared memory a cycle where there are 128; that
+// form took 700 us where this one takes 550.)  256 rows x 128 keys take about
+// 4000 cycles here, 2048 of them arithmetic: what bounds it is a group's chain,
+// about 1900 cycles of softmax and, behind it, half of PV, QK and their latency,
+// of which the other group's products cover a part.
 // The running maximum is raised, and O rescaled in tensor memory, only when a
 // tile's maximum exceeds it by more than 8 (a factor 256, which the 16-bit
 // weights and fp32 sums hold without loss of precision), i.e. hardly ever after
@@ -704,7 +723,7 @@ done:
 // (0 x NaN is not 0), scores there are masked, so K may hold anything.
 constexpr int kTile = 128;          // rows of a group's query tile
 constexpr int kKeys = ManyCut::kKeys;
-constexpr int kManyThreads = 384;   // two softmax groups, and one whose first three warps load and multiply
+constexpr int kManyThreads = 384;   // two softmax groups, and four warps of which the first loads
 // The launch's registers, 168 a thread, are shared out again: 2 x 224 + 56 = 3 x 168.
 constexpr int kSoftmaxRegs = 224, kIssueRegs = 56;
 template <int D> constexpr int kQueryBytes = kTile * D * 2;
@@ -714,8 +733,9 @@ template <int D> constexpr int kRingK = D == 128 ? 2 : 4;
 template <int D> constexpr int kRingV = D == 128 ? 3 : 6;
 template <int D> constexpr int kManySmem = 2 * kQueryBytes<D> + (kRingK<D> + kRingV<D>) * kKeyBytes<D> + 1024;
 constexpr float kRaise = 8.f;
-constexpr int kPolyOf8 = 3;   // of eight pairs of weights, how many exp2_poly takes: the special-function unit's share is
-                              // then below the products' time
+// Of eight pairs of weights, how many exp2_poly takes, so that the special-function unit, 16 results a cycle, is not
+// what both groups wait for: 0, 1, 2, 3, 4 gave 601, 585, 575, 566, 600 us with 8 units of setup, 2 and 3 are even now.
+constexpr int kPolyOf8 = 2;
 
 __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(b)), "r"(n) : "memory");
@@ -1405,8 +1425,14 @@ Region region(int way_rows, int ways, int blocks, int64_t segs, int64_t most_row
   return g;
 }
 
-// Which launch takes what.  The rows that read a key set decide: up to 16 go
-// to the few-rows kernel (its one tile), more to the many-rows kernel.
+// Which launch takes what: the rows that read a key set decide.  A sequence's
+// own keys go to the few-rows kernel up to two tiles of it (64 sequences of up
+// to 1000 keys, 8 heads of 128: 24 rows 47 us there, 57 in the many-rows kernel;
+// 32 rows 60 and 60; 64 rows 99 and 67).  The prefix goes there only if one tile
+// holds its rows: two read it twice (32 rows over 64000 keys: 106 us and 68),
+// though over a short one that costs less than the other kernel's beginning
+// (8192 keys: 28 and 32); how long it is, is known on the device alone.
+constexpr int kFewPrefix = kFewRows, kFewOwn = 2 * kFewRows;
 struct Split {
   bool few_prefix, few_own, many_prefix, many_own;
   Region few, many;
@@ -1414,9 +1440,9 @@ struct Split {
 Split split_of(int heads, int group, int n_tokens, int n, int most_q, bool with_prefix, int D) {
   Split s{};
   const int64_t p_rows = (int64_t)n_tokens * group, o_rows = (int64_t)most_q * group;
-  s.few_prefix = with_prefix && p_rows <= kFewRows;
+  s.few_prefix = with_prefix && p_rows <= kFewPrefix;
   s.many_prefix = with_prefix && !s.few_prefix;
-  s.few_own = o_rows <= kFewRows;
+  s.few_own = o_rows <= kFewOwn;
   s.many_own = !s.few_own;
   // segments of the two key sets at most, with tiles of `rows` query rows
   auto segs = [&](int rows, bool prefix, bool own) -> int64_t {

@@ -357,23 +357,25 @@ PyObject* free_slots(Args a) {
   Py_RETURN_NONE;
 }
 
-// compact(cache, table, refs) -> count: the new tables into `table` and `refs`
+// compact(cache, table, refs, into) -> (table, refs, count): the cache's own tables, or with `into` new ones like them
 PyObject* compact(Args a) {
   const CacheHandle& h = cache_of(a.v[0]);
   const c10::cuda::CUDAGuard guard(h.device);
-  const Tensor& table = a.tensor(1, "table");
-  on(table, h.device, "table");
-  if (table.scalar_type() != at::kInt || table.dim() != 2 || table.size(0) != h.c.n_slots ||
-      table.size(1) != h.c.max_pages || (table.size(1) > 1 && table.stride(1) != 1) ||
-      (table.size(0) > 1 && table.stride(0) != h.c.table_stride))
-    refuse("table must be as the cache's");
-  int32_t* refs = index_list<int32_t>(a.tensor(2, "refs"), h.device, "refs", h.c.n_pages);
+  Tensor table = a.tensor(1, "table"), refs = a.tensor(2, "refs");
+  if (a.small(3)) {
+    table = at::empty_strided(table.sizes(), table.strides(), table.options());
+    refs = make({h.c.n_pages}, at::kInt, h.device);
+  }
   const Tensor work = make({(int64_t)littlebit_cache_compact_work(h.c.n_pages)}, at::kByte, h.device);
   Tensor count = make({1}, at::kInt, h.device);
-  check(littlebit_cache_compact(&h.c, static_cast<int32_t*>(table.data_ptr()), refs,
+  check(littlebit_cache_compact(&h.c, static_cast<int32_t*>(table.data_ptr()), static_cast<int32_t*>(refs.data_ptr()),
                                 static_cast<int32_t*>(count.data_ptr()), work.data_ptr(), stream_of(h.device)),
         "littlebit_cache_compact");
-  return wrap(std::move(count));
+  PyObject* r = PyTuple_New(3);
+  PyTuple_SET_ITEM(r, 0, wrap(std::move(table)));
+  PyTuple_SET_ITEM(r, 1, wrap(std::move(refs)));
+  PyTuple_SET_ITEM(r, 2, wrap(std::move(count)));
+  return r;
 }
 
 // copy(cache, src, dst)
@@ -538,7 +540,7 @@ PyMethodDef g_methods[] = {
     {"locate", (PyCFunction)(void (*)())entry<locate, 7>, METH_FASTCALL, nullptr},
     {"fork", (PyCFunction)(void (*)())entry<fork_slots, 3>, METH_FASTCALL, nullptr},
     {"free", (PyCFunction)(void (*)())entry<free_slots, 2>, METH_FASTCALL, nullptr},
-    {"compact", (PyCFunction)(void (*)())entry<compact, 3>, METH_FASTCALL, nullptr},
+    {"compact", (PyCFunction)(void (*)())entry<compact, 4>, METH_FASTCALL, nullptr},
     {"copy", (PyCFunction)(void (*)())entry<copy_pages, 3>, METH_FASTCALL, nullptr},
     {"write", (PyCFunction)(void (*)())entry<write_rows, 9>, METH_FASTCALL, nullptr},
     {"read", (PyCFunction)(void (*)())entry<read_rows, 4>, METH_FASTCALL, nullptr},

@@ -98,6 +98,9 @@ CASES = [
     ([3, 70, 90], [7, 70], 6, 2, 16, True),                  # more new tokens than the slot holds: the first see the prefix alone
     ([2000, 1500, 2600], [1, 1], 32, 4, 16, True),
     ([600], [600], 4, 1, 1024, False),
+    ([500, 900], [4], 8, 1, 16, True),                       # two tiles of the few-rows kernel
+    ([1100, 3], [9], 16, 1, 32, True),                       # 144 rows: a wide tile, a short prefix
+    ([0, 400, 0, 300, 200], [0, 33, 0, 70], 8, 2, 64, True), # empty sequences between others
 ]
 
 
@@ -117,11 +120,10 @@ def test_attend(cm, case, width, dtype):
     assert torch.equal(got, again)
 
 
-@pytest.mark.parametrize("most", [1, 4, 64])
-def test_attend_many_sequences(cm, most):
-    """More sequences than a block has threads, in another order than their slots, some of them padding."""
+@pytest.mark.parametrize("n,most", [(300, 1), (300, 4), (300, 64), (900, 1), (900, 12)])
+def test_attend_many_sequences(cm, n, most):
+    """More sequences than a block of either kernel has threads, in another order than their slots, some of them padding."""
     rng = np.random.default_rng(most)
-    n = 300
     lengths = rng.integers(0, 40, n).tolist() + [150]
     s = Setup(cm, lengths, 1, 64, 8, torch.float16, seed=9)
     slots = rng.permutation(n)
@@ -166,6 +168,40 @@ def test_large_scores(cm, tokens):
     q = s.q(tokens, 8)
     got = s.cache.attend(q, _ints([0]), _ints([0, tokens]), prefix=1, most_q=tokens)
     s.check(got, q, [0], [0, tokens], 1)
+
+
+@pytest.mark.parametrize("tokens", [1, 60])
+@pytest.mark.parametrize("where", ["q", "k", "inf"])
+def test_non_finite_scores(cm, where, tokens):
+    """A NaN of a query spoils its own row alone, a NaN or an infinity of a key that is seen every row that sees it."""
+    s = Setup(cm, [300, 200], 1, 64, 16, torch.float16, seed=12)
+    q = s.q(tokens, 4).abs() + 0.5                           # so that the infinite key's scores are +inf
+    if where == "q":
+        q[0, 1, 3] = float("nan")
+    else:
+        page, row = int(s.cache.table[0, 2]), 5               # own key 37: before every new token
+        s.cache.planes[0][page, 0, row, 7] = float("nan") if where == "k" else float("inf")
+    got = _np(s.cache.attend(q, _ints([0]), _ints([0, tokens]), prefix=1, most_q=tokens))
+    bad = np.isnan(got)
+    if where == "q":
+        assert bad[0, 1].all() and bad.sum() == bad[0, 1].size
+    else:
+        assert bad.all()
+
+
+def test_equal_work_in_two_calls_at_once(cm):
+    """Two calls on two streams, each with its own work memory."""
+    s = Setup(cm, [500, 300, 700], 2, 128, 32, torch.bfloat16, seed=13)
+    qs = [s.q(80, 8), s.q(2, 8)]
+    lists = [(_ints([0, 1]), _ints([0, 40, 80]), 40), (_ints([0, 1]), _ints([0, 1, 2]), 1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs = [s.cache.attend(q, a, b, prefix=2, most_q=m, stream=st) for q, (a, b, m), st in zip(qs, lists, streams)]
+    torch.cuda.synchronize()
+    for out, q, (a, b, m) in zip(outs, qs, lists):
+        s.check(out, q, [0, 1], b.tolist(), 2)
 
 
 def test_a_long_cache(cm):
