@@ -486,16 +486,17 @@ struct CopyJob {
 
 // Copies the first job.rows rows of page job.src to page job.dst in every
 // plane.  An item is one (job, plane); gridDim.y blocks share it, or, where the
-// pages are small, it is one warp's, so that a thread has work for its four
-// loads under way (64 children x 64 planes of 12 KB pages: 13.9 us as
+// pages are small and many, it is one warp's, so that a thread has work for its
+// four loads under way (64 children x 64 planes of 12 KB pages: 13.9 us as
 // blocks' items, 12.8 as warps').  Rows that follow one another in memory are
 // copied as one run, so a whole page of a plain tensor is one run of all its
 // heads.  Bound by HBM for large pages, by latency for few items.
 template <class F>
 __device__ __forceinline__ void copy_items(const CopyArgs& a, int count, F job_at) {
-  const int items = count * a.n_planes, per = a.by_warp ? 32 : blockDim.x;
-  const int lane = threadIdx.x & (per - 1), worker = (int)threadIdx.x / per;
-  for (int item = blockIdx.x * (blockDim.x / per) + worker; item < items; item += gridDim.x * (blockDim.x / per)) {
+  // blocks of 256 threads: eight workers of a warp, or one
+  const int items = count * a.n_planes, per = a.by_warp ? 32 : 256, workers = a.by_warp ? 8 : 1;
+  const int lane = threadIdx.x & (per - 1), worker = a.by_warp ? threadIdx.x >> 5 : 0;
+  for (int item = blockIdx.x * workers + worker; item < items; item += gridDim.x * workers) {
     const CopyJob job = job_at(item / a.n_planes);
     if (job.dst < 0) continue;
     const PlaneDev& P = a.plane[item % a.n_planes];
@@ -770,14 +771,14 @@ CopyArgs planes_of(const lb_cache& c, int begin) {
 }
 
 // Grid of a page copy: y blocks share an item (32 KB or more each, so that
-// small pages are not cut up; pages of up to 16 KB are a warp's), and x covers
-// the items up to eight blocks an SM.
+// small pages are not cut up), and x covers the items up to eight blocks an SM.
+// Where there may be more items than that, pages of up to 16 KB are a warp's.
 dim3 copy_grid(CopyArgs& a, int64_t jobs, int page_size) {
   int64_t most = 1;
   for (int i = 0; i < a.n_planes; ++i)
     most = std::max(most, (int64_t)a.plane[i].heads * a.plane[i].row_chunks * page_size);
   const int y = (int)std::min<int64_t>(8, std::max<int64_t>(1, most / 2048));
-  a.by_warp = most <= 1024;
+  a.by_warp = most <= 1024 && jobs * a.n_planes > 148 * 8;
   const int64_t x = std::min<int64_t>(a.by_warp ? (jobs * a.n_planes + 7) / 8 : jobs * a.n_planes, 148 * 8 / y);
   return dim3((unsigned)std::max<int64_t>(1, x), (unsigned)y);
 }
