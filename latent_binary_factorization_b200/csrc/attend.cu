@@ -917,12 +917,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   unsigned char* const ks = smem + 2 * QB;   // [RK] K tiles
   unsigned char* const vs = ks + RK * KB;    // [RV] V tiles
   // k_full, v_full: a ring slot holds its tile; k_free: it has been read (both groups say so, or one twice), v_free:
-  // likewise; s_full: a group's scores are complete; o_full: a piece's last PV is done.
+  // likewise; q_full: a group's queries are in place; p_full: half of its weights; s_full: its scores are complete;
+  // o_full: a piece's last PV is done.  Every wait is bounded, also if lengths that change under way make warps disagree.
   // A parity tells whether a phase has ended only to one who knows that the phase before it has.  Within a group that
   // follows from the order of its steps.  A ring slot's last tile may have been the other group's: `loads` counts the
   // tiles whose loads have begun, and one begins only when the slot's last tile has landed and been read.
   __shared__ __align__(8) uint64_t k_full[RK], k_free[RK], v_full[RV], v_free[RV];
-  __shared__ __align__(8) uint64_t s_full[2], o_full[2];
+  __shared__ __align__(8) uint64_t q_full[2], p_full[4], s_full[2], o_full[2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t loads[2];   // of K, of V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -948,6 +949,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&v_free[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&o_full[i], 1);
     }
@@ -1030,7 +1034,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t qk = mma_shape<T>(kTile, kKeys, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
     const uint64_t q_desc = tile_desc(shared_addr(qs) + gg * QB, 16, 1024);
     uint32_t begun[2] = {0, 0};   // loads, as last seen
-    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); };
     // tile x of K (0) or V (1) is there
     auto landed = [&](int kv, uint32_t x, uint64_t* full, uint32_t parity) {
       for (int spin = 0; begun[kv] <= x && !dead; ++spin) {
@@ -1103,8 +1106,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (mine > 0) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         async_fence();
-        group_sync();
-        if (issuer) score(n + (wide ? 0 : g));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[g]);
+        if (issuer) {
+          if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&q_full[gg], pieces & 1));
+          score(n + (wide ? 0 : g));
+        }
         for (int j = 0; j < mine; ++j, ++steps) {
           const int tile = wide ? j : 2 * j + g;
           const int key = (pc.t0 + tile) * kKeys;
@@ -1189,8 +1196,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             tmem_store32(ts + 32 * half, s + 32 * half);
             tmem_store_wait();
             tc_before();
-            group_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * g + half]);
             if (issuer) {
+              if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&p_full[2 * gg + half], steps & 1));
               weigh(n + tile, j > 0, !wide, j + 1 == mine, half);
               if (half && j + 1 < mine) score(n + tile + (wide ? 1 : 2));
             }
@@ -1226,7 +1235,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
       n += tiles;
       pc = nx;
-    } while (more);   // all warps of a group walk on together, dead or not: they meet at its barrier
+    } while (more && !dead);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   if (dead) bad |= lb::kStatusTimeout;

@@ -262,9 +262,10 @@ PyObject* rotate(Args a) {
     outs[i] = given.empty() ? make(x.sizes(), dt, rope.device) : Args::as_tensor(given[i], "outs");
     dst[i] = rows_of(outs[i], rope.device, "outs", tokens, dt);
   }
-  check(littlebit_rotary(src, dst, (int)n, count_of(tokens, "positions"), ldt, pos, &rope.r, a.small(4) != 0,
-                         stream_of(rope.device)),
-        "littlebit_rotary");
+  if (tokens)   // an empty tensor has no address
+    check(littlebit_rotary(src, dst, (int)n, count_of(tokens, "positions"), ldt, pos, &rope.r, a.small(4) != 0,
+                           stream_of(rope.device)),
+          "littlebit_rotary");
   if (!given.empty()) {
     Py_INCREF(a.v[3]);
     return a.v[3];
@@ -342,6 +343,7 @@ PyObject* fork_slots(Args a) {
   const int32_t* p = index_list<int32_t>(parents, h.device, "parents", -1);
   const int n = count_of(parents.size(0), "parents");
   const int32_t* c = index_list<int32_t>(a.tensor(2, "children"), h.device, "children", n);
+  if (n == 0) Py_RETURN_NONE;
   const Tensor work = make({(int64_t)littlebit_cache_fork_work(n)}, at::kByte, h.device);
   check(littlebit_cache_fork(&h.c, p, c, n, work.data_ptr(), stream_of(h.device)), "littlebit_cache_fork");
   Py_RETURN_NONE;
@@ -353,6 +355,7 @@ PyObject* free_slots(Args a) {
   const c10::cuda::CUDAGuard guard(h.device);
   const Tensor& slots = a.tensor(1, "slots");
   const int32_t* s = index_list<int32_t>(slots, h.device, "slots", -1);
+  if (slots.size(0) == 0) Py_RETURN_NONE;
   check(littlebit_cache_free(&h.c, s, count_of(slots.size(0), "slots"), stream_of(h.device)), "littlebit_cache_free");
   Py_RETURN_NONE;
 }
@@ -386,6 +389,7 @@ PyObject* copy_pages(Args a) {
   const int32_t* s = index_list<int32_t>(src, h.device, "src", -1);
   const int n = count_of(src.size(0), "src");
   const int32_t* d = index_list<int32_t>(a.tensor(2, "dst"), h.device, "dst", n);
+  if (n == 0) Py_RETURN_NONE;
   check(littlebit_cache_copy(&h.c, s, d, n, stream_of(h.device)), "littlebit_cache_copy");
   Py_RETURN_NONE;
 }
@@ -434,7 +438,7 @@ PyObject* write_rows(Args a) {
     rope = &r.r;
   }
   if (!a.none(5)) pos = index_list<int32_t>(a.tensor(5, "positions"), h.device, "positions", tokens);
-  if ((bits || !a.none(7)) && (!rope || !pos)) refuse("rotating needs rope and positions");
+  if ((bits || !a.none(7)) && (!rope || a.none(5))) refuse("rotating needs rope and positions");
   if (a.none(7) && !a.none(8)) refuse("q_out without q");
   lb_rows q, qo;
   Tensor out;
@@ -444,9 +448,10 @@ PyObject* write_rows(Args a) {
     out = a.none(8) ? make(t.sizes(), dt, h.device) : a.tensor(8, "q_out");
     qo = rows_of(out, h.device, "q_out", tokens, dt);
   }
-  check(littlebit_cache_write(&h.c, planes.data(), src, (int)n, tokens, w, rope, pos, bits, a.none(7) ? nullptr : &q,
-                              a.none(7) ? nullptr : &qo, stream_of(h.device)),
-        "littlebit_cache_write");
+  if (tokens)
+    check(littlebit_cache_write(&h.c, planes.data(), src, (int)n, tokens, w, rope, pos, bits, a.none(7) ? nullptr : &q,
+                                a.none(7) ? nullptr : &qo, stream_of(h.device)),
+          "littlebit_cache_write");
   if (a.none(7)) Py_RETURN_NONE;
   return wrap(std::move(out));
 }
@@ -473,8 +478,9 @@ PyObject* read_rows(Args a) {
     outs[i] = given.empty() ? make({tokens, P.heads, P.width}, dt, h.device) : Args::as_tensor(given[i], "outs");
     dst[i] = rows_of(outs[i], h.device, "outs", tokens, dt);
   }
-  check(littlebit_cache_read(&h.c, planes.data(), dst, (int)n, tokens, w, stream_of(h.device)),
-        "littlebit_cache_read");
+  if (tokens)
+    check(littlebit_cache_read(&h.c, planes.data(), dst, (int)n, tokens, w, stream_of(h.device)),
+          "littlebit_cache_read");
   if (!given.empty()) {
     Py_INCREF(a.v[3]);
     return a.v[3];
@@ -500,6 +506,7 @@ PyObject* attend(Args a) {
   const double scale = a.none(8) ? 1.0 / std::sqrt((double)cq.width) : a.real(8);
   Tensor out = a.none(9) ? make(q.sizes(), q.scalar_type(), h.device) : a.tensor(9, "out");
   const lb_rows co = rows_of(out, h.device, "out", tokens, h.types[k]);
+  if (tokens == 0) return wrap(std::move(out));
   const size_t size = littlebit_cache_attend_work(&h.c, k, cq.heads, tokens, n, most_q, prefix >= 0);
   const Tensor work = make({(int64_t)size}, at::kByte, h.device);
   check(littlebit_cache_attend(&h.c, k, v, &cq, tokens, s, starts, n, prefix, most_q, (float)scale, &co,

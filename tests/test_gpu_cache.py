@@ -336,6 +336,32 @@ def test_python_refusals(cm):
         assert type(e.value).__name__ in ("ValueError", "LittleBitError"), (i, e.value)
 
 
+def test_nothing_to_do(cm):
+    """No tokens, empty lists: calls that change nothing."""
+    from latent_binary_factorization_b200 import littlebit as lb
+    c, m = _pair(cm, 8, 8, 2, 4, [(2, 64), (2, 64)])
+    none, slots, starts = _ints([]), _ints([0]), _ints([0, 0])
+    where, positions = c.extend(slots, starts, 0)
+    rows = torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")
+    rope = cm.Rotary(64)
+    assert c.write([0, 1], [rows, rows], where, rope=rope, positions=positions, rotated=[0], q=rows).shape == rows.shape
+    assert c.read([0], where)[0].shape == rows.shape
+    assert cm.rotate([rows], none, rope)[0].shape == rows.shape
+    assert c.attend(rows, slots, starts).shape == rows.shape
+    c.fork(none, none)
+    c.free(none)
+    c.copy(none, none)
+    _compare(c, m, "nothing")
+    assert lb.device_status() == 0
+
+
+def test_tensors_of_a_cache_are_read_only(cm):
+    c, _ = _pair(cm, 8, 8, 2, 4, [(2, 16)])
+    for name in ("planes", "table", "length", "refs"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+
+
 def test_another_stream(cm):
     """Calls on a stream of the caller's: their tensors belong to it."""
     s = torch.cuda.Stream()
