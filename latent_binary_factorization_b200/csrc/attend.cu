@@ -917,13 +917,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   unsigned char* const ks = smem + 2 * QB;   // [RK] K tiles
   unsigned char* const vs = ks + RK * KB;    // [RV] V tiles
   // k_full, v_full: a ring slot holds its tile; k_free: it has been read (both groups say so, or one twice), v_free:
-  // likewise; q_full: a group's queries are in place; p_full: half of its weights; s_full: its scores are complete;
-  // o_full: a piece's last PV is done.  Every wait is bounded, also if lengths that change under way make warps disagree.
+  // likewise; s_full: a group's scores are complete; o_full: a piece's last PV is done.  Every wait on them is bounded.
+  // The pieces come from the loading warp, which alone reads the lengths: msg_full, a piece is told; msg_free, all eight
+  // softmax warps have heard it.  So the warps of a group always agree on their steps, and may hand over queries and
+  // weights by named barriers, which cost half of what an mbarrier's wait does (532 us for 570 on a batch of pieces).
   // A parity tells whether a phase has ended only to one who knows that the phase before it has.  Within a group that
   // follows from the order of its steps.  A ring slot's last tile may have been the other group's: `loads` counts the
   // tiles whose loads have begun, and one begins only when the slot's last tile has landed and been read.
   __shared__ __align__(8) uint64_t k_full[RK], k_free[RK], v_full[RV], v_free[RV];
-  __shared__ __align__(8) uint64_t q_full[2], p_full[4], s_full[2], o_full[2];
+  __shared__ __align__(8) uint64_t s_full[2], o_full[2], msg_full[2], msg_free[2];
+  __shared__ Piece<ManyCut> msg[2];
+  __shared__ int msg_valid[2];   // 0: no more pieces
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t loads[2];   // of K, of V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -949,10 +953,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&v_free[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 4);
-      mbar_init(&p_full[2 * i], 4);
-      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&s_full[i], 1);
+      mbar_init(&msg_full[i], 1);
+      mbar_init(&msg_free[i], 8);
       mbar_init(&o_full[i], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -987,7 +990,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar, parity));
       };
+      uint32_t told = 0;
+      auto tell = [&](bool valid) {
+        const uint32_t i = told & 1;
+        // dead or not: a piece that not all have heard is not to be told over
+        if (told >= 2 && !__all_sync(0xffffffffu, mbar_wait(&msg_free[i], ((told >> 1) - 1) & 1))) dead = true;
+        if (lane == 0) {
+          msg[i] = pc;
+          msg_valid[i] = valid;
+          mbar_arrive(&msg_full[i]);
+        }
+        __syncwarp();
+        ++told;
+      };
       do {
+        tell(true);
         for (int t = pc.t0; t < pc.t1; ++t, ++n) {
           const int key = t * kKeys + lane * box;
           const int held = min(kKeys, pc.len - t * kKeys);
@@ -1010,6 +1027,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (lane == 0) loads[1] = n + 1;
         }
       } while (!dead && pc.next(a));
+      tell(false);
       if (dead && lane == 0) {   // copies under way land before the block ends
         for (uint32_t x = n > RK ? n - RK : 0; x < n; ++x) mbar_wait(&k_full[x % RK], (x / RK) & 1);
         for (uint32_t x = n > RV ? n - RV : 0; x < n; ++x) mbar_wait(&v_full[x % RV], (x / RV) & 1);
@@ -1017,8 +1035,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    Piece<ManyCut> pc;
-    pc.begin(a, b);
     // ---- softmax group g, this thread's row
     const int g = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
@@ -1034,6 +1050,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t qk = mma_shape<T>(kTile, kKeys, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
     const uint64_t q_desc = tile_desc(shared_addr(qs) + gg * QB, 16, 1024);
     uint32_t begun[2] = {0, 0};   // loads, as last seen
+    // Queries (0) or a half of the weights (1, 2) to the issuing warp: the others do not wait, but a dead one, whose other
+    // waits are over, does, so that no warp is ever a round ahead.
+    auto hand_over = [&](int what) {
+      if (issuer || dead) asm volatile("bar.sync %0, 128;" ::"r"(1 + 3 * g + what) : "memory");
+      else asm volatile("bar.arrive %0, 128;" ::"r"(1 + 3 * g + what) : "memory");
+    };
     // tile x of K (0) or V (1) is there
     auto landed = [&](int kv, uint32_t x, uint64_t* full, uint32_t parity) {
       for (int spin = 0; begun[kv] <= x && !dead; ++spin) {
@@ -1095,9 +1117,26 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    load_queries(pc);
-    bool more = true;
-    do {
+    // The i-th piece; false after the last.  The wait outlasts all those of the loading warp, which tells of an end in
+    // any case.
+    auto hear = [&](uint32_t i, Piece<ManyCut>& x) -> bool {
+      bool ok = false;
+      for (int k = 0; k < 16 && !ok; ++k) ok = mbar_wait(&msg_full[i & 1], (i >> 1) & 1);
+      if (!ok) {
+        dead = true;
+        return false;
+      }
+      x = msg[i & 1];
+      const bool valid = msg_valid[i & 1] != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&msg_free[i & 1]);
+      return valid;
+    };
+    uint32_t heard = 0;
+    Piece<ManyCut> pc;
+    bool more = hear(heard++, pc);
+    if (more) load_queries(pc);
+    while (more) {
       const int tiles = pc.t1 - pc.t0, mine = steps_of(pc);
       const bool wide = pc.rows_left() > kTile;
       const int at = row_of(pc);
@@ -1106,12 +1145,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (mine > 0) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         async_fence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[g]);
-        if (issuer) {
-          if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&q_full[gg], pieces & 1));
-          score(n + (wide ? 0 : g));
-        }
+        hand_over(0);
+        if (issuer) score(n + (wide ? 0 : g));
         for (int j = 0; j < mine; ++j, ++steps) {
           const int tile = wide ? j : 2 * j + g;
           const int key = (pc.t0 + tile) * kKeys;
@@ -1196,10 +1231,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             tmem_store32(ts + 32 * half, s + 32 * half);
             tmem_store_wait();
             tc_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * g + half]);
+            hand_over(1 + half);
             if (issuer) {
-              if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&p_full[2 * gg + half], steps & 1));
               weigh(n + tile, j > 0, !wide, j + 1 == mine, half);
               if (half && j + 1 < mine) score(n + tile + (wide ? 1 : 2));
             }
@@ -1208,8 +1241,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           l += sum.x + sum.y;
         }
       }
-      Piece<ManyCut> nx = pc;
-      more = nx.next(a);
+      Piece<ManyCut> nx;
+      more = hear(heard++, nx);
       if (more) load_queries(nx);
       if (mine > 0) {
         if (!dead && !mbar_wait(&o_full[g], pieces++ & 1)) dead = true;
@@ -1235,7 +1268,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
       n += tiles;
       pc = nx;
-    } while (more && !dead);
+    }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   if (dead) bad |= lb::kStatusTimeout;
