@@ -357,7 +357,8 @@ lb_status littlebit_linear_forward_noalloc(const lb_layer* layer, const void* x_
  * max_pages; LB_ERR_INDEX, a slot, page or row number outside the cache, a
  * slot twice in one list, a fork into a slot that holds tokens.  A slot number
  * of -1 in a list is padding and skipped.  Lists take up to 4096 entries.
- * Calls that change one cache must be ordered by the caller.  Alignment: every
+ * Calls that change one cache, and those that read it beside them, must be
+ * ordered by the caller.  Alignment: every
  * plane's and row tensor's base on 16 bytes, strides and row sizes multiples
  * of 16 bytes.  None of these calls allocates device memory or waits for the
  * device; their kernels use programmatic dependent launch and begin with a wait

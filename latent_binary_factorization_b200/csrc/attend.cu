@@ -453,12 +453,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   // Behind a launch of many_rows_kernel nothing of that one is needed here (it began after all work before it was
-  // done), so blocks start as its blocks leave; but the join needs both done, hence the wait at the end.
+  // done), so blocks start as its blocks leave; but the join needs both done, so the last block ends after it.
+  auto wait_last = [&]() {
+    if (a.after_many && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
   if (a.after_many) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   else lb::dependent_begin();
   const Begin b = plan_block<FewCut, kFewThreads>(a);
   if (b.u0 >= b.u1) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_last();
     return;
   }
   const uint32_t ring = shared_addr(smem) + warp * S * kFewStage<D>;
@@ -681,7 +684,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   }
 done:
   if (bad) atomicOr(a.status, bad);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_last();
 }
 
 // ------------------------------------------------------------------ many rows
