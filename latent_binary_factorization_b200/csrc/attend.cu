@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   // likewise; s_full: a group's scores are complete; o_full: a piece's last PV is done.  Every wait on them is bounded.
   // The pieces come from the loading warp, which alone reads the lengths: msg_full, a piece is told; msg_free, all eight
   // softmax warps have heard it.  So the warps of a group always agree on their steps, and may hand over queries and
-  // weights by named barriers, which cost half of what an mbarrier's wait does (532 us for 570 on a batch of pieces).
+  // weights by named barriers, which is faster than by mbarriers (550 us for 570 on a batch of pieces of prompts).
   // A parity tells whether a phase has ended only to one who knows that the phase before it has.  Within a group that
   // follows from the order of its steps.  A ring slot's last tile may have been the other group's: `loads` counts the
   // tiles whose loads have begun, and one begins only when the slot's last tile has landed and been read.
@@ -1304,14 +1304,14 @@ struct JoinArgs {
   Divisor by_group;
 };
 
-// One warp per (token, query head): finds the token's sequence, weighs the
-// row's partials of both key sets and writes the output.  Bound by latency at
-// decode sizes: the plan is one round of loads, the first eight partials another.
+// A block per token, or several where there are few tokens: finds the token's
+// sequence; then each warp takes a query head at a time, weighs the row's
+// partials of both key sets and writes the output.  Bound by latency at decode
+// sizes: the plan is one round of loads, the first six partials another.
 template <class T, int D>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
   constexpr int E = D / 32;
   const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
   __shared__ SeqPlan s_plan;
   __shared__ int s_found;
   if (threadIdx.x == 0) s_found = 0;
@@ -1329,111 +1329,114 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
     }
   }
   __syncthreads();
-  if (!s_found || h >= a.heads * a.group || head[0].width == 0 || head[1].width == 0) return;
+  if (!s_found || head[0].width == 0 || head[1].width == 0) return;
   const SeqPlan s = s_plan;
-  const int kv = a.by_group(h), sub = h - kv * a.group;
+#pragma unroll 1
+  for (int h = blockIdx.y * 8 + (threadIdx.x >> 5); h < a.heads * a.group; h += 8 * gridDim.y) {
+    const int kv = a.by_group(h), sub = h - kv * a.group;
 
-  // partials first[w], first[w] + step[w], ... (count[w] of them) of key set w, row row[w] of each
-  int first[2] = {0, 0}, step[2] = {1, 1}, count[2] = {0, 0}, at[2] = {0, 0};
+    // partials first[w], first[w] + step[w], ... (count[w] of them) of key set w, row row[w] of each
+    int first[2] = {0, 0}, step[2] = {1, 1}, count[2] = {0, 0}, at[2] = {0, 0};
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const Source& S = a.set[w];
-    if (!S.head) continue;
-    const bool few = S.few;
-    const int tile = few ? FewCut::kRows : ManyCut::kRows;
-    auto extent_of = [&](int tiles, int left) {
-      return few ? extent<FewCut>(tiles, left) : extent<ManyCut>(tiles, left);
-    };
-    // the row's segment: units ua .. ua + ext - 1
-    int row, left, r, ua, ext, seg;
-    if (w) {
-      row = (t - head[1].t0) * a.group + sub;
-      r = few ? row / FewCut::kRows : row / ManyCut::kRows;
-      left = head[1].p_rows - r * tile;
-      ua = kv * head[1].p_head + r * extent_of(head[1].p_kt, tile);
-      ext = extent_of(head[1].p_kt, left);
-      seg = kv * head[1].p_rt + r;
-    } else {
-      const int rows = s.count * a.group;
-      row = (t - s.first) * a.group + sub;
-      r = few ? row / FewCut::kRows : row / ManyCut::kRows;
-      left = rows - r * tile;
-      auto own = [&](int i) {
-        return extent_of(few ? own_tiles<FewCut>(a.by_group, rows, s.len, s.before, i)
-                             : own_tiles<ManyCut>(a.by_group, rows, s.len, s.before, i), rows - i * tile);
+    for (int w = 0; w < 2; ++w) {
+      const Source& S = a.set[w];
+      if (!S.head) continue;
+      const bool few = S.few;
+      const int tile = few ? FewCut::kRows : ManyCut::kRows;
+      auto extent_of = [&](int tiles, int left) {
+        return few ? extent<FewCut>(tiles, left) : extent<ManyCut>(tiles, left);
       };
-      int before = 0;   // units of the head's row tiles before this one
-      if (r > 0) {
-#pragma unroll 1
-        for (int i = lane; i < r; i += 32) before += own(i);
-        before = __reduce_add_sync(0xffffffffu, before);
-      }
-      ua = s.units_before + kv * s.head + before;
-      ext = own(r);
-      seg = s.segs_before + kv * (few ? up_div(rows, FewCut::kRows) : up_div(rows, ManyCut::kRows)) + r;
-    }
-    if (ext == 0) continue;
-    row -= r * tile;
-    const unsigned width = (unsigned)head[w].width;
-    const int c0 = (unsigned)ua / width, c1 = (unsigned)(ua + ext - 1) / width;
-    // few rows: one partial a block; many: the way of the row's half of a wide tile, or both ways
-    first[w] = seg + c0;
-    count[w] = c1 - c0 + 1;
-    if (!few) {
-      first[w] *= 2;
-      if (left > 128) {
-        first[w] += row >> 7;
-        row &= 127;
-        step[w] = 2;
+      // the row's segment: units ua .. ua + ext - 1
+      int row, left, r, ua, ext, seg;
+      if (w) {
+        row = (t - head[1].t0) * a.group + sub;
+        r = few ? row / FewCut::kRows : row / ManyCut::kRows;
+        left = head[1].p_rows - r * tile;
+        ua = kv * head[1].p_head + r * extent_of(head[1].p_kt, tile);
+        ext = extent_of(head[1].p_kt, left);
+        seg = kv * head[1].p_rt + r;
       } else {
-        count[w] *= 2;
-      }
-    }
-    at[w] = row;
-  }
-  float acc[E] = {}, m = -INFINITY, l = 0.f;
-  const int total = count[0] + count[1];
-  constexpr int kAtOnce = 8;
+        const int rows = s.count * a.group;
+        row = (t - s.first) * a.group + sub;
+        r = few ? row / FewCut::kRows : row / ManyCut::kRows;
+        left = rows - r * tile;
+        auto own = [&](int i) {
+          return extent_of(few ? own_tiles<FewCut>(a.by_group, rows, s.len, s.before, i)
+                               : own_tiles<ManyCut>(a.by_group, rows, s.len, s.before, i), rows - i * tile);
+        };
+        int before = 0;   // units of the head's row tiles before this one
+        if (r > 0) {
 #pragma unroll 1
-  for (int i0 = 0; i0 < total; i0 += kAtOnce) {
-    float2 p[kAtOnce];
-    float v[kAtOnce][E];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int k = i0 + i, w = k >= count[0];
-      const int x = first[w] + (k - (w ? count[0] : 0)) * step[w];
-      p[i] = make_float2(-INFINITY, 0.f);
-      if (k < total && x < a.set[w].n_partials) {
-        const long long y = (long long)x * a.set[w].rows_alloc + at[w];
-        p[i] = a.set[w].ml[y];
-        const float* src = a.set[w].part + y * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 z = *reinterpret_cast<const float4*>(src);
-          v[i][0] = z.x, v[i][1] = z.y, v[i][2] = z.z, v[i][3] = z.w;
+          for (int i = lane; i < r; i += 32) before += own(i);
+          before = __reduce_add_sync(0xffffffffu, before);
+        }
+        ua = s.units_before + kv * s.head + before;
+        ext = own(r);
+        seg = s.segs_before + kv * (few ? up_div(rows, FewCut::kRows) : up_div(rows, ManyCut::kRows)) + r;
+      }
+      if (ext == 0) continue;
+      row -= r * tile;
+      const unsigned width = (unsigned)head[w].width;
+      const int c0 = (unsigned)ua / width, c1 = (unsigned)(ua + ext - 1) / width;
+      // few rows: one partial a block; many: the way of the row's half of a wide tile, or both ways
+      first[w] = seg + c0;
+      count[w] = c1 - c0 + 1;
+      if (!few) {
+        first[w] *= 2;
+        if (left > 128) {
+          first[w] += row >> 7;
+          row &= 127;
+          step[w] = 2;
         } else {
-          const float2 z = *reinterpret_cast<const float2*>(src);
-          v[i][0] = z.x, v[i][1] = z.y;
+          count[w] *= 2;
         }
       }
+      at[w] = row;
     }
+    float acc[E] = {}, m = -INFINITY, l = 0.f;
+    const int total = count[0] + count[1];
+    constexpr int kAtOnce = 6;
+#pragma unroll 1
+    for (int i0 = 0; i0 < total; i0 += kAtOnce) {
+      float2 p[kAtOnce];
+      float v[kAtOnce][E];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (p[i].x == -INFINITY) continue;   // nothing seen; what stands in its row need not have been written
-      const float now = fmaxf(m, p[i].x);
-      const float f0 = exp2_fast(m - now), f1 = exp2_fast(p[i].x - now);
-      m = now;
-      l = l * f0 + p[i].y * f1;
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int k = i0 + i, w = k >= count[0];
+        const int x = first[w] + (k - (w ? count[0] : 0)) * step[w];
+        p[i] = make_float2(-INFINITY, 0.f);
+        if (k < total && x < a.set[w].n_partials) {
+          const long long y = (long long)x * a.set[w].rows_alloc + at[w];
+          p[i] = a.set[w].ml[y];
+          const float* src = a.set[w].part + y * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 z = *reinterpret_cast<const float4*>(src);
+            v[i][0] = z.x, v[i][1] = z.y, v[i][2] = z.z, v[i][3] = z.w;
+          } else {
+            const float2 z = *reinterpret_cast<const float2*>(src);
+            v[i][0] = z.x, v[i][1] = z.y;
+          }
+        }
+      }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + v[i][e] * f1;
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (p[i].x == -INFINITY) continue;   // nothing seen; what stands in its row need not have been written
+        const float now = fmaxf(m, p[i].x);
+        const float f0 = exp2_fast(m - now), f1 = exp2_fast(p[i].x - now);
+        m = now;
+        l = l * f0 + p[i].y * f1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f0 + v[i][e] * f1;
+      }
     }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    T r[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) r[e] = (T)(acc[e] * inv);
+    unsigned char* dst = a.out + (long long)t * a.out_token + (long long)h * a.out_head + lane * E * 2;
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(r);
+    else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(r);
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  T r[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) r[e] = (T)(acc[e] * inv);
-  unsigned char* dst = a.out + (long long)t * a.out_token + (long long)h * a.out_head + lane * E * 2;
-  if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(r);
-  else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(r);
 }
 
 // ------------------------------------------------------------------ host
@@ -1563,8 +1566,9 @@ cudaError_t launch(const Split& s, const AttendArgs& few, const AttendArgs& many
     e = lb::launch_dependent_on(st, few_rows_kernel<T, D>, dim3(s.few.blocks), kFewThreads, kFewSmem<D>, few);
   }
   if (e != cudaSuccess) return e;
-  return lb::launch_dependent_on(st, join_kernel<T, D>, dim3(join.n_tokens, lb::ceil_div(join.heads * join.group, 8)),
-                                 256, 0, join);
+  // blocks of a token: eight an SM in all, of eight heads each at least
+  const int y = std::min(lb::ceil_div(join.heads * join.group, 8), std::max(1, 148 * 8 / join.n_tokens));
+  return lb::launch_dependent_on(st, join_kernel<T, D>, dim3(join.n_tokens, y), 256, 0, join);
 }
 
 lb_status check_attend(const lb_cache* c, int k, int heads_q, int n_tokens, int n, int most_q) {
