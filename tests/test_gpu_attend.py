@@ -204,8 +204,9 @@ def test_equal_work_in_two_calls_at_once(cm):
         s.check(out, q, [0, 1], b.tolist(), 2)
 
 
-def test_a_long_cache(cm):
-    """More rows than 2^31 bytes of a plane span: offsets need 64 bits."""
+@pytest.mark.parametrize("tokens", [1, 20])
+def test_a_long_cache(cm, tokens):
+    """More rows than 2^31 bytes of a plane span: offsets need 64 bits, in both kernels."""
     page, width, n_pages = 1024, 128, 9000
     planes = [torch.empty((n_pages, 1, page, width), dtype=torch.float16, device="cuda") for _ in range(2)]
     pages = [n_pages - 1, 3, n_pages - 2]
@@ -214,11 +215,26 @@ def test_a_long_cache(cm):
     for p, x in zip(planes, (k, v)):
         p[pages] = x
     c = cm.Cache(planes, torch.tensor([pages], dtype=torch.int32, device="cuda"), _ints([2500]), _ints([0] * n_pages))
-    q = torch.randn((1, 4, width), generator=gen).half().cuda()
-    got = c.attend(q, _ints([0]), _ints([0, 1]))
+    q = torch.randn((tokens, 4, width), generator=gen).half().cuda()
+    got = c.attend(q, _ints([0]), _ints([0, tokens]), most_q=tokens)
     flat = [_np(x).reshape(1, -1, width)[:, :2500] for x in (k, v)]
-    out, reach, size = orc.attend(_np(q), lambda s: flat[0], lambda s: flat[1], [0], [0, 1])
+    out, reach, size = orc.attend(_np(q), lambda s: flat[0], lambda s: flat[1], [0], [0, tokens])
     assert (np.abs(_np(got) - out) <= orc.attend_tolerance(out, reach, size, HALF_STEP[torch.float16], width)).all()
+
+
+@pytest.mark.parametrize("lengths,tokens,hq,h,width,page", [([2500, 1100], 2500, 8, 1, 64, 16),
+                                                            ([5000, 0], 4000, 16, 4, 128, 64)])
+def test_a_long_prompt(cm, lengths, tokens, hq, h, width, page):
+    """A prompt of thousands of tokens, each seeing the ones before it: rows here and there against fp64."""
+    s = Setup(cm, lengths, h, width, page, torch.bfloat16, seed=14)
+    q = s.q(tokens, hq)
+    got = s.cache.attend(q, _ints([0]), _ints([0, tokens]), prefix=1, most_q=tokens)
+    for t in (0, 1, 15, 16, 31, 127, 128, 1000, 1999, tokens - 2, tokens - 1):
+        seen = lengths[0] - tokens + t + 1
+        k, v = ({0: x[0][:, :seen], 1: x[1]}.__getitem__ for x in (s.k, s.v))
+        out, reach, size = orc.attend(_np(q[t: t + 1]), k, v, [0], [0, 1], 1)
+        tol = orc.attend_tolerance(out, reach, size, HALF_STEP[torch.bfloat16], width)
+        assert (np.abs(_np(got[t: t + 1]) - out) <= tol).all(), t
 
 
 @pytest.mark.parametrize("most", [1, 100])
