@@ -9,7 +9,9 @@
 // Bookkeeping (extend, fork, compact) is decided by one block of 1024 threads:
 // the decisions are a scan over the lists and over refs[], a few KB to a few
 // hundred KB, where a second block would only add a grid-wide wait.  The rows
-// that move afterwards are copied by a grid of their own.
+// that move afterwards are copied by a grid of their own.  Each decision takes
+// 3 to 4 us at decode sizes, a chain of about six trips to L2 (slots, lengths,
+// claims and back, references, tables).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -111,7 +113,8 @@ struct Item {
 // two 16-byte loads, the rotation in fp32, and as many stores.  One item a
 // thread at a time: eight blocks an SM hide the latency, and two or four items
 // a thread cost more in registers than they bring (a rotary prompt of 2048
-// tokens x 72 heads, bf16: 18.4 us with one, 19.8 with two, 33 with four).
+// tokens x 72 heads, bf16: 18.5 us with one, 19.8 with two, 33 with four).  4096
+// tokens of 64 + 8 + 8 heads written: 31 us, 5.4 TB/s, 82 % of the copy rate.
 template <class T>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowArgs a) {
   constexpr int E = 16 / sizeof(T);
