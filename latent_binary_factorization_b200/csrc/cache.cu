@@ -493,7 +493,8 @@ struct CopyJob {
 // four loads under way (64 children x 64 planes of 12 KB pages: 13.9 us as
 // blocks' items, 12.8 as warps').  Rows that follow one another in memory are
 // copied as one run, so a whole page of a plain tensor is one run of all its
-// heads.  Bound by HBM for large pages, by latency for few items.
+// heads.  Bound by HBM for large pages (about 470 of 2048 pages moved in 16 planes
+// of 64 KB pages: 169 us, 5.7 TB/s), by latency for few items.
 template <class F>
 __device__ __forceinline__ void copy_items(const CopyArgs& a, int count, F job_at) {
   // blocks of 256 threads: eight workers of a warp, or one
