@@ -12,6 +12,7 @@ All calls take ``stream`` (a torch.cuda.Stream, default the current one of the
 tensors' device); tensors that a call makes belong to that stream.  What the
 bookkeeping cannot do (no free page, an index outside the cache) is left out
 and reported by ``littlebit.device_status()``, bits 1 << 8 and 1 << 9.
+Autograd does not see these calls.
 """
 from __future__ import annotations
 
@@ -77,7 +78,7 @@ def rotate(xs: list, positions: torch.Tensor, rope: Rotary, outs: list | None = 
     """Rotated rows of up to eight tensors (tokens, heads, width), fp16, bf16 or
     fp32, one dtype, in one launch.  ``outs`` may be ``xs`` (in place).
     inverse turns back; with any scale it is also the transpose, i.e. the
-    gradient of the rotation (autograd does not see these calls)."""
+    gradient of the rotation."""
     if stream is not None:
         with _on(stream, rope.device):
             return _b.rotate(rope._h, xs, positions, outs, inverse)
@@ -102,7 +103,8 @@ class Cache:
     @classmethod
     def empty(cls, shapes: list, n_pages: int, page_size: int, n_slots: int, max_pages: int, dtype=torch.float16,
               device="cuda") -> "Cache":
-        """A new empty cache; shapes: (heads, width) of every plane."""
+        """A new empty cache; shapes: (heads, width) of every plane, whose
+        contents are undefined until they are written."""
         planes = [torch.empty((n_pages, h, page_size, w), dtype=dtype, device=device) for h, w in shapes]
         return cls(planes, torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros(n_slots, dtype=torch.int32, device=device),
