@@ -311,8 +311,8 @@ __device__ __forceinline__ int claim_value(int n, int i) { return -(n - i); }
 // ------------------------------------------------------------------ extend
 
 __global__ void __launch_bounds__(kBookThreads, 1)
-    extend_kernel(const Tables c, const int* __restrict__ slots, const int* __restrict__ starts, int n, int n_tokens,
-                  int prefix, long long* __restrict__ where, int* __restrict__ positions) {
+    extend_kernel(const Tables c, const int* slots, const int* starts, int n, int n_tokens,
+                  int prefix, long long* where, int* positions) {
   extern __shared__ int sm[];
   int* s_start = sm;              // [n + 1]
   int* s_len = s_start + n + 1;   // [n] tokens before the call; -1: not extended
@@ -420,9 +420,9 @@ __global__ void __launch_bounds__(kBookThreads, 1)
 }
 
 __global__ void __launch_bounds__(256)
-    locate_kernel(const Tables c, const int* __restrict__ slots, const int* __restrict__ starts,
-                  const int* __restrict__ begin, int n, int n_tokens, int prefix, long long* __restrict__ where,
-                  int* __restrict__ positions) {
+    locate_kernel(const Tables c, const int* slots, const int* starts,
+                  const int* begin, int n, int n_tokens, int prefix, long long* where,
+                  int* positions) {
   lb::dependent_begin();
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= n_tokens) return;
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(256)
   positions[t] = p;
 }
 
-__global__ void __launch_bounds__(128) free_kernel(const Tables c, const int* __restrict__ slots) {
+__global__ void __launch_bounds__(128) free_kernel(const Tables c, const int* slots) {
   lb::dependent_begin();
   const int s = slots[blockIdx.x];
   if (s < 0 || s >= c.n_slots) {
@@ -546,8 +546,8 @@ struct ForkJob {
 };
 
 __global__ void __launch_bounds__(kBookThreads, 1)
-    fork_kernel(const Tables c, const int* __restrict__ parents, const int* __restrict__ children, int n,
-                ForkJob* __restrict__ fork, CopyJob* __restrict__ copy) {
+    fork_kernel(const Tables c, const int* parents, const int* children, int n,
+                ForkJob* fork, CopyJob* copy) {
   extern __shared__ int sm[];
   int* s_len = sm;            // [n] tokens of the parent; -1: left out
   int* s_off = s_len + n;     // [n]
@@ -617,8 +617,8 @@ __global__ void __launch_bounds__(kBookThreads, 1)
 
 // Blocks y = 0 first share out the children's table rows, then all copy the last pages.
 __global__ void __launch_bounds__(256)
-    fork_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, const ForkJob* __restrict__ fork,
-                     const CopyJob* __restrict__ copy, int n, int with_tables) {
+    fork_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, const ForkJob* fork,
+                     const CopyJob* copy, int n, int with_tables) {
   lb::dependent_begin();
   if (with_tables && blockIdx.y == 0)
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
@@ -638,8 +638,8 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ compact
 
 __global__ void __launch_bounds__(kBookThreads, 1)
-    compact_kernel(const Tables c, int* refs_out, int* __restrict__ count_out, CopyJob* __restrict__ jobs,
-                   int* __restrict__ moved, int* __restrict__ n_jobs) {
+    compact_kernel(const Tables c, int* refs_out, int* count_out, CopyJob* jobs,
+                   int* moved, int* n_jobs) {
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
   lb::dependent_begin();
@@ -695,8 +695,8 @@ __global__ void __launch_bounds__(kBookThreads, 1)
 
 __global__ void __launch_bounds__(256)
     compact_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, int* table_out,
-                        const int* __restrict__ count, const CopyJob* __restrict__ jobs,
-                        const int* __restrict__ moved, const int* __restrict__ n_jobs, int with_tables) {
+                        const int* count, const CopyJob* jobs,
+                        const int* moved, const int* n_jobs, int with_tables) {
   lb::dependent_begin();
   if (with_tables) {
     const int live = *count;
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(256)
-    copy_kernel(const __grid_constant__ CopyArgs a, const int* __restrict__ src, const int* __restrict__ dst, int n,
+    copy_kernel(const __grid_constant__ CopyArgs a, const int* src, const int* dst, int n,
                 int n_pages) {
   lb::dependent_begin();
   copy_items(a, n, [&](int i) {

@@ -247,7 +247,10 @@ unsigned int* noalloc_status_word(int dev);
 // Programmatic dependent launch of the paged cache's kernels: each may be
 // scheduled while the stream's previous kernel ends, and waits for that one's
 // writes before it touches memory.  Every one of them calls dependent_begin()
-// first, so that its end implies the end of all work before it.
+// first, so that its end implies the end of all work before it.  None of them
+// takes a const __restrict__ pointer: that promises data that nobody writes
+// while the kernel runs, which lets its loads pass the wait, and the kernel
+// before may still be running.
 #ifdef __CUDACC__
 __device__ __forceinline__ void dependent_begin() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
