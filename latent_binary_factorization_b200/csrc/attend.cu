@@ -925,7 +925,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   unsigned char* const ks = smem + 2 * QB;   // [RK] K tiles
   unsigned char* const vs = ks + RK * KB;    // [RV] V tiles
   // k_full, v_full: a ring slot holds its tile; k_free: it has been read (both groups say so, or one twice), v_free:
-  // likewise; s_full: a group's scores are complete; o_full: a piece's last PV is done.  Every wait on them is bounded.
+  // likewise; s_full: a group's scores are complete; o_full: a piece's last PV is done; quiet: all products of a group
+  // that gave up are.  Every wait on them is bounded.
   // The pieces come from the loading warp, which alone reads the lengths: msg_full, a piece is told; msg_free, all eight
   // softmax warps have heard it.  So the warps of a group always agree on their steps, and may hand over queries and
   // weights by named barriers, which is faster than by mbarriers (550 us for 570 on a batch of pieces of prompts).
@@ -933,7 +934,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   // follows from the order of its steps.  A ring slot's last tile may have been the other group's: `loads` counts the
   // tiles whose loads have begun, and one begins only when the slot's last tile has landed and been read.
   __shared__ __align__(8) uint64_t k_full[RK], k_free[RK], v_full[RV], v_free[RV];
-  __shared__ __align__(8) uint64_t s_full[2], o_full[2], msg_full[2], msg_free[2];
+  __shared__ __align__(8) uint64_t s_full[2], o_full[2], msg_full[2], msg_free[2], quiet[2];
   __shared__ Piece<ManyCut> msg[2];
   __shared__ int msg_valid[2];   // 0: no more pieces
   __shared__ uint32_t tmem_slot;
@@ -965,6 +966,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&msg_full[i], 1);
       mbar_init(&msg_free[i], 8);
       mbar_init(&o_full[i], 1);
+      mbar_init(&quiet[i], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1036,9 +1038,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
       } while (!dead && pc.next(a));
       tell(false);
-      if (dead && lane == 0) {   // copies under way land before the block ends
-        for (uint32_t x = n > RK ? n - RK : 0; x < n; ++x) mbar_wait(&k_full[x % RK], (x / RK) & 1);
-        for (uint32_t x = n > RV ? n - RV : 0; x < n; ++x) mbar_wait(&v_full[x % RV], (x / RV) & 1);
+      if (dead && lane == 0) {   // copies under way land before the block ends: all begun, of K perhaps one more than of V
+        const uint32_t k = loads[0], v = loads[1];
+        for (uint32_t x = k > RK ? k - RK : 0; x < k; ++x) mbar_wait(&k_full[x % RK], (x / RK) & 1);
+        for (uint32_t x = v > RV ? v - RV : 0; x < v; ++x) mbar_wait(&v_full[x % RV], (x / RV) & 1);
       }
     }
   } else {
@@ -1130,7 +1133,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     auto hear = [&](uint32_t i, Piece<ManyCut>& x) -> bool {
       bool ok = false;
       for (int k = 0; k < 16 && !ok; ++k) ok = mbar_wait(&msg_full[i & 1], (i >> 1) & 1);
-      if (!ok) {
+      if (!__all_sync(0xffffffffu, ok)) {
         dead = true;
         return false;
       }
@@ -1278,6 +1281,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       pc = nx;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (dead && issuer) {   // products under way end before the block does (in a block that is well, o_full said so)
+      if (elect_one()) tc_commit(&quiet[gg]);
+      __syncwarp();
+      mbar_wait(&quiet[gg], 0);
+    }
   }
   if (dead) bad |= lb::kStatusTimeout;
   if (bad) atomicOr(a.status, bad);

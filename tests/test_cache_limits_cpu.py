@@ -20,3 +20,18 @@ def test_dependent_kernels_promise_nothing_about_their_inputs(name):
     code = re.sub(r"//.*", "", _source(name))
     assert "dependent_begin" in code
     assert "__restrict__" not in code and "__ldg" not in code and "ld.global.nc" not in code
+
+
+def test_a_block_that_gave_up_waits_for_all_that_it_began():
+    """The many-rows kernel's way out after a wait that ran out cannot be run
+    without a hang, so its source is looked at: it drains both rings up to the
+    copies that were begun (of K one more than of V may be), and the products."""
+    code = _source("attend.cu")
+    ring = code[code.index("if (dead && lane == 0)"):]
+    ring = ring[: ring.index("\n      }\n")]
+    assert re.search(r"k = loads\[0\], v = loads\[1\]", ring)
+    assert re.search(r"x < k; \+\+x\) mbar_wait\(&k_full", ring) and re.search(r"x < v; \+\+x\) mbar_wait\(&v_full", ring)
+    out = code[code.index("if (dead && issuer)"):]
+    out = out[: out.index("\n    }\n")]
+    assert "tc_commit(&quiet[gg])" in out and "mbar_wait(&quiet[gg], 0)" in out
+    assert code.index("if (dead && issuer)") < code.index("tcgen05.dealloc")
