@@ -707,20 +707,25 @@ done:
 //   others: the groups have the same rows and take every other key tile.
 // Each group leaves a partial of its own, so a slot has two `ways`.
 //
-// Tensor memory, of each group: S (fp32, 128 columns), whose first 64 columns
-// then hold P (16-bit pairs), and O (fp32, D columns): all 512 for D = 128.
+// Tensor memory, of each group: S (fp32, 128 columns), P (16-bit pairs, 64) and
+// O (fp32, D).  For D = 128 there is room for two of them only, and P lies in
+// the first 64 columns of S.
 // A group is one chain, S(i) -> softmax -> PV(i) -> QK(i + 1), and while one is
 // in its softmax the other's products run; PV starts when half of P is there.
 // The group's first warp issues its products: a warp of their own had to be
 // woken for each, and took 700 us for 626.
-// The tensor core takes a group's products in order, so S(i + 1) being complete
-// means that PV(i) is, and no barrier guards P or O.  (Tiles of 64 keys with P
-// beside S, whose QK(i + 1) runs beside softmax i, have a shorter chain but fetch
-// Q twice as often, 192 bytes of shared memory a cycle where there are 128; that
-// form took 700 us where this one takes 550.)  256 rows x 128 keys take about
-// 4000 cycles here, 2048 of them arithmetic: what bounds it is a group's chain,
-// about 1900 cycles of softmax and, behind it, half of PV, QK and their latency,
-// of which the other group's products cover a part.
+// A commit tells that all products issued before it are complete, so S(i + 1)
+// being there means that PV(i) is, and P and O may be written.  Products with
+// different accumulators are promised no order among themselves, though: where
+// QK(i + 1) writes over the P that PV(i) reads (D = 128), it is issued when PV(i)
+// is complete.  On a batch of pieces of prompts that costs 603 us for 586.
+// (Issuing the keys whose scores miss P before it, in products half as wide: 625.
+// Tiles of 64 keys with P beside S, whose QK(i + 1) runs beside softmax i, have a
+// shorter chain but fetch Q twice as often, 192 bytes of shared memory a cycle
+// where there are 128; that form took 700 us where this one took 550.)
+// 256 rows x 128 keys take about 4000 cycles here, 2048 of them arithmetic: what
+// bounds it is a group's chain, about 1900 cycles of softmax and, behind it, half
+// of PV, QK and their latency, of which the other group's products cover a part.
 // Measured: 16 pieces of up to 130 tokens over a prefix of 12000, 64 query heads
 // on 8, bf16: 540 us with the join, 848 TFLOP/s; 4096 tokens of 32 heads over
 // 23000 keys, fp16: 853 TFLOP/s.
@@ -739,6 +744,8 @@ template <int D> constexpr int kKeyBytes = kKeys * D * 2;
 // K and V tiles in flight (a K tile is done with half a step earlier).
 template <int D> constexpr int kRingK = D == 128 ? 2 : 4;
 template <int D> constexpr int kRingV = D == 128 ? 3 : 6;
+// First column of P, counted from its group's S: its first, or those that a narrow O leaves.
+template <int D> constexpr int kWeights = D == 128 ? 0 : 256 + D;
 template <int D> constexpr int kManySmem = 2 * kQueryBytes<D> + (kRingK<D> + kRingV<D>) * kKeyBytes<D> + 1024;
 constexpr float kRaise = 8.f;
 // Of eight pairs of weights, how many exp2_poly takes, so that the special-function unit, 16 results a cycle, is not
@@ -925,8 +932,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   unsigned char* const ks = smem + 2 * QB;   // [RK] K tiles
   unsigned char* const vs = ks + RK * KB;    // [RV] V tiles
   // k_full, v_full: a ring slot holds its tile; k_free: it has been read (both groups say so, or one twice), v_free:
-  // likewise; s_full: a group's scores are complete; o_full: a piece's last PV is done; quiet: all products of a group
-  // that gave up are.  Every wait on them is bounded.
+  // likewise; s_full: a group's scores are complete; p_free: its PV is, another QK follows over its P; o_full: a piece's
+  // last PV is done; quiet: all products of a group that gave up are.  Every wait on them is bounded.
   // The pieces come from the loading warp, which alone reads the lengths: msg_full, a piece is told; msg_free, all eight
   // softmax warps have heard it.  So the warps of a group always agree on their steps, and may hand over queries and
   // weights by named barriers, which is faster than by mbarriers (550 us for 570 on a batch of pieces of prompts).
@@ -934,7 +941,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   // follows from the order of its steps.  A ring slot's last tile may have been the other group's: `loads` counts the
   // tiles whose loads have begun, and one begins only when the slot's last tile has landed and been read.
   __shared__ __align__(8) uint64_t k_full[RK], k_free[RK], v_full[RV], v_free[RV];
-  __shared__ __align__(8) uint64_t s_full[2], o_full[2], msg_full[2], msg_free[2], quiet[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_free[2], o_full[2], msg_full[2], msg_free[2], quiet[2];
   __shared__ Piece<ManyCut> msg[2];
   __shared__ int msg_valid[2];   // 0: no more pieces
   __shared__ uint32_t tmem_slot;
@@ -966,6 +973,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&msg_full[i], 1);
       mbar_init(&msg_free[i], 8);
       mbar_init(&o_full[i], 1);
+      mbar_init(&p_free[i], 1);
       mbar_init(&quiet[i], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1049,13 +1057,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // ---- softmax group g, this thread's row
     const int g = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane0 = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + 128 * g + lane0, to = tmem + 256 + 128 * g + lane0;
+    const uint32_t ts = tmem + 128 * g + lane0, tp = ts + kWeights<D>, to = ts + 256;
     const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);   // above 0, so that -inf stays -inf
     // The group's first warp issues its products, one elected lane of it; what is uniform for the warp (tm, gg) is
     // made so for the compiler, so that the descriptors live in uniform registers.
     const bool issuer = (warp & 3) == 0;
     const uint32_t gg = __shfl_sync(0xffffffffu, (uint32_t)g, 0);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + 128 * gg;   // S and P; O 256 columns on
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + 128 * gg;   // S; O 256 columns on
     constexpr uint32_t pv = mma_shape<T>(kTile, D, true);
     // a negative scale negates the queries, so that the softmax knows positive ones only
     const uint32_t qk = mma_shape<T>(kTile, kKeys, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
@@ -1076,9 +1084,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(full, parity));
       tc_after();
     };
-    // tile x: S = Q K^T
-    auto score = [&](uint32_t x) {
+    uint32_t turns = 0;   // waits on p_free
+    // tile x: S = Q K^T; `after`: behind a PV of the same piece
+    auto score = [&](uint32_t x, bool after) {
       landed(0, x, &k_full[x % RK], (x / RK) & 1);
+      if (!kWeights<D> && after && !dead) {
+        dead = !__all_sync(0xffffffffu, mbar_wait(&p_free[gg], turns++ & 1));
+        tc_after();
+      }
       const uint64_t k = tile_desc(shared_addr(ks) + x % RK * KB, 16, 1024);
       if (elect_one()) {
 #pragma unroll
@@ -1096,11 +1109,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < kKeys / 32; ++c)
-          mma_ts(tm + 256, tm + 8 * (c + 4 * half), v + (c + 4 * half) * 2048 / 16, pv, add || c + half > 0);
+          mma_ts(tm + 256, tm + kWeights<D> + 8 * (c + 4 * half), v + (c + 4 * half) * 2048 / 16, pv, add || c + half > 0);
         if (half) {
           tc_commit(&v_free[x % RV]);
           if (once) mbar_arrive(&v_free[x % RV]);
           if (last) tc_commit(&o_full[gg]);
+          else if (!kWeights<D>) tc_commit(&p_free[gg]);
         }
       }
       __syncwarp();
@@ -1157,7 +1171,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         async_fence();
         hand_over(0);
-        if (issuer) score(n + (wide ? 0 : g));
+        if (issuer) score(n + (wide ? 0 : g), false);
         for (int j = 0; j < mine; ++j, ++steps) {
           const int tile = wide ? j : 2 * j + g;
           const int key = (pc.t0 + tile) * kKeys;
@@ -1239,13 +1253,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                 s[i0 + i] = Mma<T>::pack(e.x, e.y);
               }
             }
-            tmem_store32(ts + 32 * half, s + 32 * half);
+            tmem_store32(tp + 32 * half, s + 32 * half);
             tmem_store_wait();
             tc_before();
             hand_over(1 + half);
             if (issuer) {
               weigh(n + tile, j > 0, !wide, j + 1 == mine, half);
-              if (half && j + 1 < mine) score(n + tile + (wide ? 1 : 2));
+              if (half && j + 1 < mine) score(n + tile + (wide ? 1 : 2), true);
             }
           }
           const float2 sum = split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));

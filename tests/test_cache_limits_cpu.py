@@ -35,3 +35,22 @@ def test_a_block_that_gave_up_waits_for_all_that_it_began():
     out = out[: out.index("\n    }\n")]
     assert "tc_commit(&quiet[gg])" in out and "mbar_wait(&quiet[gg], 0)" in out
     assert code.index("if (dead && issuer)") < code.index("tcgen05.dealloc")
+
+
+def test_scores_do_not_rely_on_the_order_of_products():
+    """Products with different accumulators are promised no order: where P
+    shares S's columns, the next scores' products follow a wait for the PV
+    that reads it; where it does not, the columns of S, O and P are disjoint."""
+    code = _source("attend.cu")
+    score = code[code.index("auto score = "):]
+    score = score[: score.index("mma_ss(")]
+    assert "if (!kWeights<D> && after && !dead)" in score and "mbar_wait(&p_free[gg]" in score
+    at = {128: 0, 64: 256 + 64}                              # kWeights
+    assert "kWeights = D == 128 ? 0 : 256 + D" in code
+    for d, p in at.items():
+        used = []
+        for g in range(2):
+            used += [*range(128 * g, 128 * g + 128), *range(256 + 128 * g, 256 + 128 * g + d)]
+            if p:
+                used += range(128 * g + p, 128 * g + p + 64)
+        assert len(used) == len(set(used)) and max(used) < 512
