@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(256)
     CopyJob j{src[i], dst[i], a.page_size, 0};
     if (j.src == -1 && j.dst == -1) return j;   // padding
     if (j.src < 0 || j.src >= n_pages || j.dst < 0 || j.dst >= n_pages) {
-      if (threadIdx.x == 0) atomicOr(&g_status, kStatusIndex);
+      if ((threadIdx.x & 31) == 0) atomicOr(&g_status, kStatusIndex);   // an item may be any warp's
       j.dst = -1;
     }
     return j;
