@@ -193,14 +193,17 @@ class Cache:
 
     # ---- attention
     def attend(self, q: torch.Tensor, slots: torch.Tensor, starts: torch.Tensor, k: int = 0, v: int = 1,
-               prefix: int = -1, most_q: int = 1, scale: float | None = None, out: torch.Tensor | None = None,
-               stream=None) -> torch.Tensor:
+               prefix: int = -1, most_q: int | None = None, scale: float | None = None,
+               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of the newest tokens over slot ``prefix`` (shared by the
         whole batch, read once for it) and their own slots.  q: (tokens, query
         heads, width), sequence i holding its rows starts[i] .. starts[i+1],
         the last tokens of slots[i], each of which sees the prefix and its own
-        slot up to itself.  most_q bounds the tokens of one sequence.  k and v:
-        planes (fp16 or bf16, width 64 or 128).  scale: default width^-0.5.
+        slot up to itself.  most_q: the tokens of the longest of these sequences,
+        which decides how the work is done, not what comes out (default: their
+        mean, right for steps of single tokens and for prompts of one size).
+        k and v: planes (fp16 or bf16, width 64 or 128).  scale: default
+        width^-0.5.
         Rows in no sequence are left as ``out`` has them (undefined in one made
         here)."""
         if stream is not None:

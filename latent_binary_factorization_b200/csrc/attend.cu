@@ -15,10 +15,12 @@
 // segments lie in a row of U units, and with W = ceil(U / grid) block c takes
 // units [c W, (c + 1) W): every block gets the same amount of work whatever the
 // lengths.  A block writes one fp32 partial for each segment that it touches,
-// at slot segment + c (unique, since along the row of units one of the two grows
-// from partial to partial), and join_kernel adds a row's partials in the order
-// of their blocks: the result does not depend on timing.  The lengths are read
-// on the device, so a captured graph follows a growing cache.
+// its rows from row R + c kRows of the work memory on, R being the rows of the
+// segments before and kRows the most that a segment has (along the row of units
+// R grows by a segment's rows or c by one from partial to partial, so no two
+// meet), and join_kernel adds a row's partials in the order of their blocks: the
+// result does not depend on timing.  The lengths are read on the device, so a
+// captured graph follows a growing cache.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,13 +41,26 @@ constexpr unsigned kStatusIndex = 1u << LB_ERR_INDEX;
 // measured: with 3, 5, 6, 9 and 12 a batch of pieces of prompts (16 sequences of
 // up to 130 tokens over a prefix of 12000, each with own keys) took 727, 560,
 // 551, 557 and 566 us, as its short segments end late or early.
+// `stored`: rows of a partial of a segment whose query rows end `left` from its
+// first: those of a narrow tile of many_rows_kernel come in two ways, 128 apart.
 struct FewCut {
   static constexpr int kRows = 16, kKeys = 64, kSetup = 1;
+  static __host__ __device__ constexpr int stored(int left) { return left < 16 ? left : 16; }
 };
 struct ManyCut {
   static constexpr int kRows = 256, kKeys = 128, kSetup = 6;
+  static __host__ __device__ constexpr int stored(int left) { return left > 256 ? 256 : left > 128 ? left : 128 + left; }
 };
+// Of all segments of `rows` query rows.
+template <class C>
+__host__ __device__ constexpr int stored_rows(int rows) {
+  const int full = rows / C::kRows * C::kRows;   // kRows: a power of two
+  return rows > full ? full + C::stored(rows - full) : full;
+}
 constexpr int kMaxUnits = 0x7fffffff;
+// More stored rows than any call has (2^29 + 2^24 by its limits): sums end here, so that lists whose starts descend, and
+// overlap, cannot wrap them.
+constexpr int kMaxStored = 1 << 30;
 
 using lb::Divisor;
 
@@ -65,7 +80,7 @@ struct PlanHead {
 };
 struct SeqPlan {
   int units_before;   // units of the launch before this sequence's (the prefix's included)
-  int segs_before;    // segments before this sequence's (the prefix's included)
+  int rows_before;    // stored rows before this sequence's (the prefix's included)
   int first, count;   // tokens
   int len, before;    // see Seq
   int head;           // units of one head's segments
@@ -82,7 +97,7 @@ struct AttendArgs {
   int n_pages, page_shift, n_slots, max_pages;
   const int* slots;
   const int* starts;
-  int n, n_tokens, prefix, most_q;
+  int n, n_tokens, prefix;
   int heads, group;            // K and V heads; query heads of each
   Divisor by_group;
   float scale_log2;
@@ -90,9 +105,9 @@ struct AttendArgs {
   int after_many;              // the launch before is many_rows_kernel of the same call
   PlanHead* head;              // written by block 0 for the join
   SeqPlan* seqs;
-  float2* ml;                  // [partial][rows_alloc] maximum (times log2 e) and sum
-  float* part;                 // [partial][rows_alloc][D]
-  int rows_alloc, n_partials;
+  float2* ml;                  // [n_rows] maximum (times log2 e) and sum
+  float* part;                 // [n_rows][D]
+  int n_rows;                  // below kMaxStored
   unsigned* status;
 };
 
@@ -116,7 +131,7 @@ __device__ __forceinline__ uint32_t shared_addr(const void* p) {
 // ------------------------------------------------------------------ the plan
 
 struct Seq {
-  int first, count;   // tokens of the batch (count cut to most_q)
+  int first, count;   // tokens of the batch
   int len;            // keys
   int before;         // keys before the first of the tokens: token j sees before + j + 1 of them
   int slot;
@@ -129,8 +144,8 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int i) {
   const int end = min(max(a.starts[i + 1], s.first), a.n_tokens);
   const bool ok = s.slot >= 0 && s.slot < a.n_slots;
   s.len = ok ? min(max(a.length[s.slot], 0), a.max_pages << a.page_shift) : 0;
-  s.before = s.len - (end - s.first);
-  s.count = min(end - s.first, a.most_q);
+  s.count = end - s.first;
+  s.before = s.len - s.count;
   return s;
 }
 
@@ -163,7 +178,7 @@ struct Begin {
   int p_rt, p_kt, p_rows, p_head, p_len, t0;
   int seq;                   // sequence of u0; -1: the prefix
   int seq_u;                 // units before it
-  int seq_segs;              // segments before it
+  int seq_rows;              // stored rows before it
 };
 
 // Run by the whole block (THREADS threads): a sweep over the sequences, THREADS
@@ -174,11 +189,11 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ long long warp_u[W];
-  __shared__ int warp_s[W], found[3];   // sequence, units before, segments before
+  __shared__ int warp_s[W], found[3];              // sequence, units before, stored rows before
   Begin b;
-  long long p_units = 0, u = 0;         // the sums are taken in 64 bits, and used if they fit 31
-  int segs = 0;
-  // this thread's sequence of the step: its units, and those and the segments before it
+  long long p_units = 0, u = 0;         // the sums of units are taken in 64 bits, and used if they fit 31
+  int stored = 0;
+  // this thread's sequence of the step: its units, and those and the stored rows before it
   long long mine = 0, before_u = 0;
   int before_s = 0;
   auto step = [&](int i0, bool leave) {
@@ -189,7 +204,7 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
     if (i < a.n) {
       s = load_seq(a, i);
       const int rows = s.count * a.group;
-      mine_s = up_div(rows, C::kRows) * a.heads;
+      mine_s = stored_rows<C>(rows) * a.heads;
       head = own_head<C>(a.by_group, rows, s.len, s.before);
       mine = (long long)head * a.heads;
       if (leave && s.slot != -1 && (s.slot < 0 || s.slot >= a.n_slots)) atomicOr(a.status, kStatusIndex);
@@ -202,7 +217,7 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
       const int ys = __shfl_up_sync(0xffffffffu, xs, d);
       if (lane >= d) {
         xu += yu;
-        xs += ys;
+        xs = min(xs + ys, kMaxStored);
       }
     }
     __syncthreads();
@@ -212,15 +227,15 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
     }
     __syncthreads();
     before_u = u + xu - mine;
-    before_s = segs + xs - mine_s;
+    before_s = min(stored + (xs - mine_s), kMaxStored);
 #pragma unroll 1
     for (int w = 0; w < W; ++w) {
       if (w < warp) {
         before_u += warp_u[w];
-        before_s += warp_s[w];
+        before_s = min(before_s + warp_s[w], kMaxStored);
       }
       u += warp_u[w];
-      segs += warp_s[w];
+      stored = min(stored + warp_s[w], kMaxStored);
     }
     if (leave && i < a.n)
       a.seqs[i] = SeqPlan{(int)min(before_u, (long long)kMaxUnits), before_s, s.first, s.count, s.len, s.before, head, 0};
@@ -243,9 +258,9 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
   }
   b.p_head = (int)min(p_units, (long long)kMaxUnits);
   p_units *= a.heads;
-  const int p_segs = b.p_rt * a.heads, n = a.do_own ? a.n : 0;
+  const int p_stored = stored_rows<C>(b.p_rows) * a.heads, n = a.do_own ? a.n : 0;
   u = p_units;
-  segs = p_segs;
+  stored = p_stored;
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += THREADS) step(i0, blockIdx.x == 0);
 
@@ -255,18 +270,18 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
   b.u0 = (int)min((long long)width * blockIdx.x, u);
   b.u1 = (int)min((long long)width * (blockIdx.x + 1), u);
   b.seq = -1;
-  b.seq_u = b.seq_segs = 0;
+  b.seq_u = b.seq_rows = 0;
   if (blockIdx.x == 0 && tid == 0) {
     *a.head = PlanHead{width, b.t0, t1, b.p_rows, b.p_rt, b.p_kt, b.p_head, 0};
     if (!fits) atomicOr(a.status, kStatusIndex);
   }
   if (b.u0 < p_units || b.u0 >= b.u1) return b;
   u = p_units;
-  segs = p_segs;
+  stored = p_stored;
   if (n > THREADS && tid == 0) {   // lengths that changed since the first sweep may leave u0 without a place
     found[0] = 0;
     found[1] = b.u0;
-    found[2] = p_segs;
+    found[2] = p_stored;
   }
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += THREADS) {
@@ -280,7 +295,7 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
   __syncthreads();
   b.seq = found[0];
   b.seq_u = found[1];
-  b.seq_segs = found[2];
+  b.seq_rows = found[2];
   return b;
 }
 
@@ -291,7 +306,7 @@ template <class C>
 struct Piece {
   int seq;                   // -1: the prefix
   int h, r;                  // head, row tile
-  int seg;                   // segment number
+  unsigned row0;             // stored rows of the segments before
   int rows;                  // query rows of the key set
   int first, len, before;    // first token; keys; keys before the first token
   const int* table;          // page table row
@@ -350,7 +365,7 @@ struct Piece {
       ++r;
       e = ext(a);
     }
-    seg = b.seq_segs + h * rt + r;
+    row0 = b.seq_rows + h * stored_rows<C>(rows) + r * C::kRows;
     cut(x, e);
   }
   __device__ __forceinline__ bool next(const AttendArgs& a) {
@@ -358,7 +373,7 @@ struct Piece {
     int e;
 #pragma unroll 1
     do {
-      ++seg;
+      row0 += C::stored(rows_left());
       ++r;
       if (rows_left() <= 0) {
         r = 0;
@@ -520,7 +535,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
   float m[2], l[2];
   int lim[2];   // keys that rows g and g + 8 see
   int stage = 0, ahead = 0, t = 0;      // ahead: copies begun, up to S - 1
-  int slot = 0, rows = 0;
+  int row0 = 0, rows = 0;               // of the piece's partial
   bool fresh = true, begun = false;     // fresh: a new piece
   for (;;) {
     if (fresh) {
@@ -529,11 +544,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       for (;;) {
         if (begun && !w.next(a)) goto done;
         begun = true;
-        slot = w.seg + (int)blockIdx.x;
-        rows = slot < a.n_partials ? min(min(kFewRows, a.rows_alloc), w.rows_left()) : 0;
+        row0 = w.row0 + blockIdx.x * kFewRows;
+        rows = (unsigned)row0 <= (unsigned)(a.n_rows - kFewRows) ? min(kFewRows, w.rows_left()) : 0;
         if (w.t0 < w.t1) break;
         // units of the segment's beginning only
-        if (threadIdx.x < rows) a.ml[(long long)slot * a.rows_alloc + threadIdx.x] = make_float2(-INFINITY, 0.f);
+        if (threadIdx.x < rows) a.ml[row0 + threadIdx.x] = make_float2(-INFINITY, 0.f);
       }
       t = w.t0;
 #pragma unroll
@@ -652,7 +667,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
       if (top != -INFINITY)
 #pragma unroll
         for (int x = 0; x < 4; ++x) sum += exp2_fast(stat[x][threadIdx.x].x - top) * stat[x][threadIdx.x].y;
-      a.ml[(long long)slot * a.rows_alloc + threadIdx.x] = make_float2(top, sum);
+      a.ml[row0 + threadIdx.x] = make_float2(top, sum);
     }
 #pragma unroll
     for (int half = 0; half < D / 64; ++half) {
@@ -677,7 +692,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_rows_kernel(const __grid_c
             v.z += y.z;
             v.w += y.w;
           }
-          *reinterpret_cast<float4*>(a.part + ((long long)slot * a.rows_alloc + row) * D + half * 64 + col) = v;
+          *reinterpret_cast<float4*>(a.part + (long long)(row0 + row) * D + half * 64 + col) = v;
         }
       }
       __syncthreads();
@@ -705,7 +720,8 @@ done:
 //   wide segments (more than 128 rows): the groups have different rows and
 //   share every K and V tile, which halves what has to come out of L2;
 //   others: the groups have the same rows and take every other key tile.
-// Each group leaves a partial of its own, so a slot has two `ways`.
+// Each group leaves a partial of its own, which in a narrow segment makes two
+// `ways` of the same rows.
 //
 // Tensor memory, of each group: S (fp32, 128 columns), P (16-bit pairs, 64) and
 // O (fp32, D).  For D = 128 there is room for two of them only, and P lies in
@@ -1275,11 +1291,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         tc_after();
       }
       // ---- the partial: rows of one way, or two ways of the same rows
-      const long long slot = (pc.seg + (long long)blockIdx.x) * 2 + g;
-      const bool keep = at < pc.rows && row < a.rows_alloc && slot < a.n_partials;
-      if (keep) a.ml[slot * a.rows_alloc + row] = make_float2(m, l);
+      const unsigned first = pc.row0 + blockIdx.x * ManyCut::kRows, to_row = first + g * kTile + row;
+      const bool keep = at < pc.rows && first <= (unsigned)(a.n_rows - ManyCut::kRows);
+      if (keep) a.ml[to_row] = make_float2(m, l);
       if (mine > 0) {
-        float* dst = a.part + (slot * a.rows_alloc + row) * D;
+        float* dst = a.part + (long long)to_row * D;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -1321,7 +1337,7 @@ struct Source {
   const float2* ml;
   const float* part;
   int few;                    // of few_rows_kernel, else of many_rows_kernel
-  int rows_alloc, n_partials;
+  int n_rows;
 };
 struct JoinArgs {
   Source set[2];   // the own keys', the prefix's (head null: no prefix)
@@ -1362,8 +1378,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   for (int h = blockIdx.y * 8 + (threadIdx.x >> 5); h < a.heads * a.group; h += 8 * gridDim.y) {
     const int kv = a.by_group(h), sub = h - kv * a.group;
 
-    // partials first[w], first[w] + step[w], ... (count[w] of them) of key set w, row row[w] of each
-    int first[2] = {0, 0}, step[2] = {1, 1}, count[2] = {0, 0}, at[2] = {0, 0};
+    // rows first[w], first[w] + step[w], ... (count[w] of them) of the work memory are the row's partials in key set w
+    int first[2] = {0, 0}, step[2] = {1, 1}, count[2] = {0, 0};
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const Source& S = a.set[w];
@@ -1374,14 +1390,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
         return few ? extent<FewCut>(tiles, left) : extent<ManyCut>(tiles, left);
       };
       // the row's segment: units ua .. ua + ext - 1
-      int row, left, r, ua, ext, seg;
+      int row, left, r, ua, ext, before;   // before: stored rows before the head's
       if (w) {
         row = (t - head[1].t0) * a.group + sub;
         r = few ? row / FewCut::kRows : row / ManyCut::kRows;
         left = head[1].p_rows - r * tile;
         ua = kv * head[1].p_head + r * extent_of(head[1].p_kt, tile);
         ext = extent_of(head[1].p_kt, left);
-        seg = kv * head[1].p_rt + r;
+        before = kv * (few ? stored_rows<FewCut>(head[1].p_rows) : stored_rows<ManyCut>(head[1].p_rows));
       } else {
         const int rows = s.count * a.group;
         row = (t - s.first) * a.group + sub;
@@ -1391,34 +1407,24 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
           return extent_of(few ? own_tiles<FewCut>(a.by_group, rows, s.len, s.before, i)
                                : own_tiles<ManyCut>(a.by_group, rows, s.len, s.before, i), rows - i * tile);
         };
-        int before = 0;   // units of the head's row tiles before this one
+        int units = 0;   // of the head's row tiles before this one
         if (r > 0) {
 #pragma unroll 1
-          for (int i = lane; i < r; i += 32) before += own(i);
-          before = __reduce_add_sync(0xffffffffu, before);
+          for (int i = lane; i < r; i += 32) units += own(i);
+          units = __reduce_add_sync(0xffffffffu, units);
         }
-        ua = s.units_before + kv * s.head + before;
+        ua = s.units_before + kv * s.head + units;
         ext = own(r);
-        seg = s.segs_before + kv * (few ? up_div(rows, FewCut::kRows) : up_div(rows, ManyCut::kRows)) + r;
+        before = s.rows_before + kv * (few ? stored_rows<FewCut>(rows) : stored_rows<ManyCut>(rows));
       }
       if (ext == 0) continue;
-      row -= r * tile;
       const unsigned width = (unsigned)head[w].width;
       const int c0 = (unsigned)ua / width, c1 = (unsigned)(ua + ext - 1) / width;
-      // few rows: one partial a block; many: the way of the row's half of a wide tile, or both ways
-      first[w] = seg + c0;
-      count[w] = c1 - c0 + 1;
-      if (!few) {
-        first[w] *= 2;
-        if (left > 128) {
-          first[w] += row >> 7;
-          row &= 127;
-          step[w] = 2;
-        } else {
-          count[w] *= 2;
-        }
-      }
-      at[w] = row;
+      // one partial a block, in a narrow tile of many_rows_kernel two ways of it; tiles before the row's are full
+      first[w] = before + row + c0 * tile;
+      const bool ways = !few && left <= 128;
+      step[w] = ways ? tile / 2 : tile;
+      count[w] = ways ? 2 * (c1 - c0 + 1) : c1 - c0 + 1;
     }
     float acc[E] = {}, m = -INFINITY, l = 0.f;
     const int total = count[0] + count[1];
@@ -1432,10 +1438,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
         const int k = i0 + i, w = k >= count[0];
         const int x = first[w] + (k - (w ? count[0] : 0)) * step[w];
         p[i] = make_float2(-INFINITY, 0.f);
-        if (k < total && x < a.set[w].n_partials) {
-          const long long y = (long long)x * a.set[w].rows_alloc + at[w];
-          p[i] = a.set[w].ml[y];
-          const float* src = a.set[w].part + y * D + lane * E;
+        if (k < total && (unsigned)x < (unsigned)a.set[w].n_rows) {
+          p[i] = a.set[w].ml[x];
+          const float* src = a.set[w].part + (long long)x * D + lane * E;
           if constexpr (E == 4) {
             const float4 z = *reinterpret_cast<const float4*>(src);
             v[i][0] = z.x, v[i][1] = z.y, v[i][2] = z.z, v[i][3] = z.w;
@@ -1481,22 +1486,22 @@ int sm_count() {
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
-// Work memory of one launch: [head][sequences][ml][partials].
+// Work memory of one launch: [head][sequences][ml][partials], for `rows` stored
+// rows and a further tile for every block's beginning within a segment.
 struct Region {
-  int blocks, rows_alloc, ways;   // blocks 0: no such launch
-  long long partials;
+  int blocks, few;   // blocks 0: no such launch
+  long long rows;
   size_t seqs, ml, part, bytes;
 };
-Region region(int way_rows, int ways, int blocks, int64_t segs, int64_t most_rows, int n, int D) {
+Region region(int tile, int blocks, int64_t rows, int n, int D) {
   Region g;
   g.blocks = blocks;
-  g.rows_alloc = (int)std::min<int64_t>(way_rows, most_rows);
-  g.ways = ways;
-  g.partials = (segs + blocks) * ways;
+  g.few = tile == kFewRows;
+  g.rows = rows + (int64_t)tile * blocks;
   g.seqs = up(sizeof(PlanHead));
   g.ml = g.seqs + up(sizeof(SeqPlan) * (size_t)n);
-  g.part = g.ml + up(sizeof(float2) * (size_t)g.partials * g.rows_alloc);
-  g.bytes = g.part + up(sizeof(float) * (size_t)g.partials * g.rows_alloc * D);
+  g.part = g.ml + up(sizeof(float2) * (size_t)g.rows);
+  g.bytes = g.part + up(sizeof(float) * (size_t)g.rows * D);
   return g;
 }
 
@@ -1506,7 +1511,10 @@ Region region(int way_rows, int ways, int blocks, int64_t segs, int64_t most_row
 // 32 rows 60 and 60; 64 rows 99 and 67).  The prefix goes there only if one tile
 // holds its rows: two read it twice (32 rows over 64000 keys: 106 us and 68),
 // though over a short one that costs less than the other kernel's beginning
-// (8192 keys: 28 and 32); how long it is, is known on the device alone.
+// (8192 keys: 28 and 32); how long it is, is known on the device alone.  So are the
+// tokens of each sequence: most_q decides by what the caller knows, and either
+// kernel takes any number, so the work memory has room for any division of the
+// batch's tokens.
 constexpr int kFewPrefix = kFewRows, kFewOwn = 2 * kFewRows;
 struct Split {
   bool few_prefix, few_own, many_prefix, many_own;
@@ -1519,19 +1527,14 @@ Split split_of(int heads, int group, int n_tokens, int n, int most_q, bool with_
   s.many_prefix = with_prefix && !s.few_prefix;
   s.few_own = o_rows <= kFewOwn;
   s.many_own = !s.few_own;
-  // segments of the two key sets at most, with tiles of `rows` query rows
-  auto segs = [&](int rows, bool prefix, bool own) -> int64_t {
-    const int64_t one = (o_rows + rows - 1) / rows;
-    return (int64_t)heads * ((prefix ? (p_rows + rows - 1) / rows : 0) +
-                             (own ? std::min<int64_t>(n * one, n + (p_rows + rows - 1) / rows) : 0));
-  };
+  // Stored rows at most: one for each query row, and in the many-rows kernel 128 more for a narrow last tile, which
+  // the prefix and every sequence may have.
   if (s.few_prefix || s.few_own)
-    s.few = region(kFewRows, 1, 2 * sm_count(), segs(kFewRows, s.few_prefix, s.few_own),
-                   std::max(s.few_prefix ? p_rows : 0, s.few_own ? o_rows : 0), n, D);
-  if (s.many_prefix || s.many_own) {
-    const int64_t most = std::max(s.many_prefix ? p_rows : 0, s.many_own ? o_rows : 0);
-    s.many = region(kTile, 2, sm_count(), segs(ManyCut::kRows, s.many_prefix, s.many_own), most, n, D);
-  }
+    s.few = region(kFewRows, 2 * sm_count(), heads * p_rows * ((int)s.few_prefix + (int)s.few_own), n, D);
+  if (s.many_prefix || s.many_own)
+    s.many = region(ManyCut::kRows, sm_count(),
+                    heads * ((s.many_prefix ? p_rows + 128 : 0) + (s.many_own ? p_rows + 128ll * std::min(n, n_tokens) : 0)),
+                    n, D);
   return s;
 }
 
@@ -1645,7 +1648,6 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   most_q = std::min(most_q, n_tokens);
   const Split s = split_of(K.heads, group, n_tokens, n, most_q, prefix >= 0, D);
   if (work_bytes < s.few.bytes + s.many.bytes) return LB_ERR_SHAPE;
-  if (s.few.partials > INT32_MAX || s.many.partials > INT32_MAX) return LB_ERR_SHAPE;
   CUtensorMap map_k{}, map_v{};
   if (s.many.blocks && ((r = plane_map(*c, K, &map_k)) != LB_OK || (r = plane_map(*c, V, &map_v)) != LB_OK)) return r;
   unsigned* status = nullptr;
@@ -1670,7 +1672,6 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   a.n = n;
   a.n_tokens = n_tokens;
   a.prefix = prefix;
-  a.most_q = most_q;
   a.heads = K.heads;
   a.group = group;
   a.by_group = lb::divisor(group);
@@ -1685,9 +1686,8 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
     x.seqs = reinterpret_cast<SeqPlan*>(w + g.seqs);
     x.ml = reinterpret_cast<float2*>(w + g.ml);
     x.part = reinterpret_cast<float*>(w + g.part);
-    x.rows_alloc = g.rows_alloc;
-    x.n_partials = (int)g.partials;
-    const Source src{x.head, x.seqs, x.ml, x.part, g.ways == 1, g.rows_alloc, (int)g.partials};
+    x.n_rows = (int)g.rows;
+    const Source src{x.head, x.seqs, x.ml, x.part, g.few, (int)g.rows};
     if (own) j.set[0] = src;
     if (with_prefix) j.set[1] = src;
     return x;

@@ -490,12 +490,12 @@ PyObject* read_rows(Args a) {
   return r;
 }
 
-// attend(cache, q, slots, starts, k, v, prefix, most_q, scale or None, out or None) -> out
+// attend(cache, q, slots, starts, k, v, prefix, most_q or None, scale or None, out or None) -> out
 PyObject* attend(Args a) {
   const CacheHandle& h = cache_of(a.v[0]);
   const c10::cuda::CUDAGuard guard(h.device);
   const Tensor& q = a.tensor(1, "q");
-  const int k = a.small(4), v = a.small(5), prefix = a.small(6), most_q = a.small(7);
+  const int k = a.small(4), v = a.small(5), prefix = a.small(6);
   if (k < 0 || k >= h.c.n_planes || v < 0 || v >= h.c.n_planes) refuse("k and v must be planes of the cache");
   const lb_rows cq = rows_of(q, h.device, "q", -1, h.types[k]);
   const int tokens = count_of(q.size(0), "q");
@@ -503,6 +503,7 @@ PyObject* attend(Args a) {
   const int32_t* s = index_list<int32_t>(slots, h.device, "slots", -1);
   const int n = count_of(slots.size(0), "slots");
   const int32_t* starts = index_list<int32_t>(a.tensor(3, "starts"), h.device, "starts", n + 1ll);
+  const int most_q = !a.none(7) ? a.small(7) : n > 0 && tokens > 0 ? (tokens - 1) / n + 1 : 1;   // None: the mean
   const double scale = a.none(8) ? 1.0 / std::sqrt((double)cq.width) : a.real(8);
   Tensor out = a.none(9) ? make(q.sizes(), q.scalar_type(), h.device) : a.tensor(9, "out");
   const lb_rows co = rows_of(out, h.device, "out", tokens, h.types[k]);

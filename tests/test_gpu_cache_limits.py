@@ -30,6 +30,10 @@ def _ints(v):
     return torch.tensor([int(x) for x in v], dtype=torch.int32, device="cuda")
 
 
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
 def _randn(shape, dtype, seed):
     return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
 
@@ -38,6 +42,32 @@ def _cache(cm, n_pages, page, n_slots, max_pages, shapes, seed=0, dtype=torch.fl
     planes = [_randn((n_pages, h, page, w), dtype, seed + i) for i, (h, w) in enumerate(shapes)]
     return cm.Cache(planes, torch.full((n_slots, max_pages), -1, dtype=torch.int32, device="cuda"), _ints([0] * n_slots),
                     _ints([0] * n_pages))
+
+
+HALF_STEP = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+
+
+class Sequences:
+    """Slots of the given lengths in pages of random order, with the fp64 rows that they hold."""
+
+    def __init__(self, cm, lengths, heads, width, page, dtype, seed=0):
+        need = [-(-n // page) for n in lengths]
+        self.cache = _cache(cm, sum(need) + 2, page, len(lengths), max(need + [1]), [(heads, width)] * 2, seed, dtype)
+        order = np.random.default_rng(seed).permutation(sum(need) + 2)
+        self.rows, at = ({}, {}), 0
+        for s, n in enumerate(lengths):
+            pages = order[at: at + need[s]].tolist()
+            at += need[s]
+            self.cache.table[s, : need[s]] = _ints(pages)
+            for plane, rows in zip(self.cache.planes, self.rows):
+                rows[s] = _np(plane[pages].transpose(0, 1).reshape(heads, -1, width)[:, :n])
+        self.cache.length.copy_(_ints(lengths))
+        self.dtype, self.width = dtype, width
+
+    def check(self, got, q, slots, starts, prefix=-1):
+        out, reach, size = orc.attend(_np(q), self.rows[0].__getitem__, self.rows[1].__getitem__, slots, starts, prefix)
+        tol = orc.attend_tolerance(out, reach, size, HALF_STEP[self.dtype], self.width)
+        assert (np.abs(_np(got) - out) <= tol).all()
 
 
 # ------------------------------------------------------------------ page copies
@@ -57,3 +87,42 @@ def test_a_bad_page_among_many_copies_is_reported(cm, status, planes, at):
     c.copy(_ints(src), _ints(dst))
     assert status() == orc.INDEX
     assert all(torch.equal(p, w) for p, w in zip(c.planes, want))
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("most_q", [None, 1, 2, 40, 1000])
+@pytest.mark.parametrize("new,heads_q,heads", [([40, 130, 1], 4, 2), ([40, 130, 1], 8, 1), ([1, 1, 33, 1, 1, 1], 16, 2),
+                                               ([300], 2, 2), ([2, 2], 4, 4)])
+@pytest.mark.parametrize("with_prefix", [False, True])
+def test_most_q_decides_no_output(cm, status, new, heads_q, heads, most_q, with_prefix):
+    """However long the sequences are said to be (None: nothing is said), every token gets its output."""
+    lengths = [n + 17 * i for i, n in enumerate(new)] + [90]
+    s = Sequences(cm, lengths, heads, 64, 16, torch.float16, seed=len(new))
+    starts = np.concatenate(([0], np.cumsum(new)))
+    q = _randn((int(starts[-1]), heads_q, 64), torch.float16, 3)
+    prefix = len(new) if with_prefix else -1
+    out = torch.full_like(q, float("nan"))
+    s.cache.attend(q, _ints(range(len(new))), _ints(starts), prefix=prefix, most_q=most_q, out=out)
+    s.check(out, q, list(range(len(new))), starts, prefix)
+    assert status() == 0
+
+
+def test_a_prompt_without_most_q_is_not_cut(cm):
+    """The call as it is written without the argument."""
+    s = Sequences(cm, [70], 2, 128, 16, torch.bfloat16)
+    q = _randn((70, 8, 128), torch.bfloat16, 4)
+    s.check(s.cache.attend(q, _ints([0]), _ints([0, 70])), q, [0], [0, 70])
+
+
+@pytest.mark.parametrize("most_q", [1, 5000])
+def test_a_long_prompt_said_to_be_short(cm, most_q):
+    """Thousands of tokens in the kernel for few rows, and single tokens in the one for many."""
+    s = Sequences(cm, [3000, 700, 700], 1, 64, 64, torch.float16, seed=5)
+    q = _randn((2002, 4, 64), torch.float16, 6)
+    got = s.cache.attend(q, _ints([0, 1, 2]), _ints([0, 2000, 2001, 2002]), prefix=-1, most_q=most_q)
+    for t in (0, 1, 15, 16, 500, 1998, 1999):
+        one = Sequences.__new__(Sequences)
+        one.rows = [{0: r[0][:, : 1000 + t + 1]} for r in s.rows]
+        one.dtype, one.width = s.dtype, s.width
+        one.check(got[t: t + 1], q[t: t + 1], [0], [0, 1])
+    s.check(got[2000:], q[2000:], [1, 2], [0, 1, 2])
