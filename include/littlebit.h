@@ -351,8 +351,8 @@ lb_status littlebit_linear_forward_noalloc(const lb_layer* layer, const void* x_
  * Everything the bookkeeping calls decide lies in device memory, so a serving
  * step of them may be captured into a CUDA graph.  They allocate the
  * lowest-numbered free pages, in the order of the lists given.  What cannot be
- * done is left out as a whole (a sequence is not extended, a child not made)
- * and raises a bit in the cache status word of the device, which
+ * done is left out as a whole (a sequence is not extended, a child not made),
+ * takes nothing from what follows it in the list, and raises a bit in the cache status word of the device, which
  * littlebit_device_status returns: LB_ERR_PAGES, no free page or no room in
  * max_pages; LB_ERR_INDEX, a slot, page or row number outside the cache, a
  * slot twice in one list, a fork into a slot that holds tokens.  A slot number

@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kBookThreads, 1)
   extern __shared__ int sm[];
   int* s_start = sm;              // [n + 1]
   int* s_len = s_start + n + 1;   // [n] tokens before the call; -1: not extended
-  int* s_off = s_len + n;         // [n] first of the new pages; -1 entries are marked in s_len
+  int* s_off = s_len + n;         // [n] new pages, then those of the sequences before
   int* s_slot = s_off + n;        // [n]
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
@@ -376,29 +376,51 @@ __global__ void __launch_bounds__(kBookThreads, 1)
     s_off[i] = need;
   }
   __syncthreads();
-  const int want = scan_list(s_off, n, warp_sums);
-  const int found = take_free(c.refs, c.n_pages, want, warp_sums, [&](int rank, int page) {
-    const int i = owner_of(s_off, n, rank);
-    c.table[s_slot[i] * c.table_stride + pages_of(s_len[i], c) + rank - s_off[i]] = page;
-    c.refs[page] = 1;
-  });
-  __syncthreads();
-  for (int i = tid; i < n; i += kBookThreads) {
-    if (s_len[i] < 0) continue;
-    const int need = (i + 1 < n ? s_off[i + 1] : want) - s_off[i];
-    if (need > 0 && s_off[i] + need > found) {   // give back what was taken
+  auto take = [&](int want) {
+    return take_free(c.refs, c.n_pages, want, warp_sums, [&](int rank, int page) {
+      const int i = owner_of(s_off, n, rank);
+      c.table[s_slot[i] * c.table_stride + pages_of(s_len[i], c) + rank - s_off[i]] = page;
+      c.refs[page] = 1;
+    });
+  };
+  const int want = scan_list(s_off, n, warp_sums), found = take(want);
+  if (found < want) {
+    // Too few: all are given back, the sequences that do not fit what those before them leave are refused, one after
+    // another (rare; 166 us for 4096), and the others take theirs.
+    __syncthreads();
+    for (int i = tid; i < n; i += kBookThreads) {
+      if (s_len[i] < 0) continue;
+      const int need = (i + 1 < n ? s_off[i + 1] : want) - s_off[i];
       for (int k = 0; k < need && s_off[i] + k < found; ++k) {
         int* e = &c.table[s_slot[i] * c.table_stride + pages_of(s_len[i], c) + k];
         c.refs[*e] = 0;
         *e = -1;
       }
-      c.length[s_slot[i]] = s_len[i];
-      s_len[i] = -1;
-      bad |= kStatusPages;
-    } else {
-      c.length[s_slot[i]] = s_len[i] + count(i);
     }
+    __syncthreads();
+    for (int i = tid; i < n; i += kBookThreads)
+      s_off[i] = s_len[i] < 0 ? 0
+                              : (int)(((long long)s_len[i] + count(i) + c.page_size - 1) >> c.page_shift) - pages_of(s_len[i], c);
+    __syncthreads();
+    if (tid == 0) {
+      int left = found;
+      for (int i = 0; i < n; ++i) {
+        if (s_off[i] <= left) {
+          left -= s_off[i];
+        } else {
+          c.length[s_slot[i]] = s_len[i];
+          s_len[i] = -1;
+          s_off[i] = 0;
+          bad |= kStatusPages;
+        }
+      }
+    }
+    __syncthreads();
+    take(scan_list(s_off, n, warp_sums));
   }
+  __syncthreads();
+  for (int i = tid; i < n; i += kBookThreads)
+    if (s_len[i] >= 0) c.length[s_slot[i]] = s_len[i] + count(i);
   __syncthreads();
   int shift = 0;
   if (prefix >= 0) shift = max(c.length[prefix], 0);

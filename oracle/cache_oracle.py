@@ -93,10 +93,10 @@ class Model:
                 self.status |= PAGES
                 continue
             need = self.pages(length + n) - self.pages(length)
-            asked += need
-            if need and asked > len(free):
+            if asked + need > len(free):   # asks for nothing then: those behind may still fit
                 self.status |= PAGES
                 continue
+            asked += need
             for k in range(need):
                 page = free[asked - need + k]
                 self.table[s, self.pages(length) + k] = page

@@ -6,6 +6,7 @@ import re
 import pytest
 
 from latent_binary_factorization_b200 import build_ext
+from oracle import cache_oracle as orc
 
 
 def _source(name):
@@ -54,3 +55,10 @@ def test_scores_do_not_rely_on_the_order_of_products():
             if p:
                 used += range(128 * g + p, 128 * g + p + 64)
         assert len(used) == len(set(used)) and max(used) < 512
+
+
+def test_oracle_a_refused_sequence_asks_for_nothing():
+    m = orc.Model(3, 8, 3, 16)
+    where, _ = m.extend([0, 1, 2], [0, 80, 88, 93], 93)
+    assert m.status == orc.PAGES and m.length.tolist() == [0, 8, 5]
+    assert where[80:].tolist() == [*range(8), *range(8, 13)] and (where[:80] == -1).all()

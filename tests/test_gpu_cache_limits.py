@@ -89,6 +89,50 @@ def test_a_bad_page_among_many_copies_is_reported(cm, status, planes, at):
     assert all(torch.equal(p, w) for p, w in zip(c.planes, want))
 
 
+# ------------------------------------------------------------------ too few pages
+def _same(c, m):
+    for name in ("table", "length", "refs"):
+        assert np.array_equal(getattr(c, name).cpu().numpy(), getattr(m, name)), name
+
+
+def test_a_refused_sequence_takes_no_pages_from_others(cm, status):
+    """Three pages are free: the sequence that asks for ten is left out, and the two behind it get theirs."""
+    c = _cache(cm, 3, 8, 3, 16, [(1, 8)])
+    where, positions = c.extend(_ints([0, 1, 2]), _ints([0, 80, 88, 93]), 93)
+    assert status() == orc.PAGES
+    assert c.length.tolist() == [0, 8, 5] and c.refs.tolist() == [1, 1, 0]
+    assert where.tolist() == [-1] * 80 + list(range(8)) + list(range(8, 13))
+    assert positions.tolist() == [-1] * 80 + list(range(8)) + list(range(5))
+
+
+@pytest.mark.parametrize("n_pages,n_slots,most", [(7, 5, 30), (40, 30, 60), (5000, 2500, 60), (9000, 4096, 100)])
+def test_shortages_follow_the_model(cm, status, n_pages, n_slots, most):
+    """Steps that ask for more than there is, of sequences with and without a partly filled page, a slot named twice and
+    padding among them: who gets pages, which, and what stays as it was."""
+    rng = np.random.default_rng(n_pages)
+    c = _cache(cm, n_pages, 8, n_slots, 16, [(1, 8)])
+    m = orc.Model(n_pages, 8, n_slots, 16)
+    short = 0
+    for step in range(8):
+        slots = rng.permutation(n_slots)
+        slots[rng.random(n_slots) < 0.1] = -1
+        slots[-1] = slots[0]
+        grow = rng.integers(0, 3, n_slots) * rng.integers(0, most, n_slots)
+        starts = np.concatenate(([0], np.cumsum(grow)))
+        tokens = int(starts[-1])
+        got = c.extend(_ints(slots), _ints(starts), tokens, prefix=0)
+        want = m.extend(slots.tolist(), starts.tolist(), tokens, prefix=0)
+        assert all(np.array_equal(g.cpu().numpy(), w) for g, w in zip(got, want)), step
+        _same(c, m)
+        assert status() == m.status, step
+        short += bool(m.status & orc.PAGES) and not c.refs.eq(0).any().item()
+        m.status = 0
+        gone = rng.permutation(n_slots)[: n_slots // 3].tolist()
+        c.free(_ints(gone))
+        m.free(gone)
+    assert short   # some step took the last page
+
+
 # ------------------------------------------------------------------ attention
 @pytest.mark.parametrize("most_q", [None, 1, 2, 40, 1000])
 @pytest.mark.parametrize("new,heads_q,heads", [([40, 130, 1], 4, 2), ([40, 130, 1], 8, 1), ([1, 1, 33, 1, 1, 1], 16, 2),
