@@ -742,6 +742,9 @@ done:
 // 256 rows x 128 keys take about 4000 cycles here, 2048 of them arithmetic: what
 // bounds it is a group's chain, about 1900 cycles of softmax and, behind it, half
 // of PV, QK and their latency, of which the other group's products cover a part.
+// (All powers of two come from the special-function unit: an eighth or a quarter
+// of them by a polynomial on the multiply-add units, exact to 2^-22.5, took 599
+// and 602 us for 594.)
 // Measured: 16 pieces of up to 130 tokens over a prefix of 12000, 64 query heads
 // on 8, bf16: 540 us with the join, 848 TFLOP/s; 4096 tokens of 32 heads over
 // 23000 keys, fp16: 853 TFLOP/s.
@@ -764,9 +767,6 @@ template <int D> constexpr int kRingV = D == 128 ? 3 : 6;
 template <int D> constexpr int kWeights = D == 128 ? 0 : 256 + D;
 template <int D> constexpr int kManySmem = 2 * kQueryBytes<D> + (kRingK<D> + kRingV<D>) * kKeyBytes<D> + 1024;
 constexpr float kRaise = 8.f;
-// Of eight pairs of weights, how many exp2_poly takes, so that the special-function unit, 16 results a cycle, is not
-// what both groups wait for: 0, 1, 2, 3, 4 gave 601, 585, 575, 566, 600 us with 8 units of setup, 2 and 3 are even now.
-constexpr int kPolyOf8 = 2;
 
 __device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(b)), "r"(n) : "memory");
@@ -902,22 +902,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-// 2^x of two values of at most 2^7 on the multiply-add units: x = n + r with n the nearest whole number (the sum with
-// 1.5 * 2^23 rounds to it), 2^r by the polynomial of degree 4 with the smallest largest relative error on [-1/2, 1/2]
-// (2.6e-6, by Remez exchange), and n added to the exponent.  Below -126: about 2^-126.
-__device__ __forceinline__ float2 exp2_poly(uint64_t x) {
-  float2 v = split(x);
-  const uint64_t c = pair(fmaxf(v.x, -126.f), fmaxf(v.y, -126.f));
-  const uint64_t t = add2(c, pair(12582912.f, 12582912.f));
-  const uint64_t r = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), c);
-  uint64_t p = fma2(r, pair(0.009570102207362652f, 0.009570102207362652f), pair(0.05591785907745361f, 0.05591785907745361f));
-  p = fma2(p, r, pair(0.240247443318367f, 0.240247443318367f));
-  p = fma2(p, r, pair(0.6931217908859253f, 0.6931217908859253f));
-  p = fma2(p, r, pair(0.9999992847442627f, 0.9999992847442627f));
-  const float2 q = split(p), n = split(t);
-  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
-                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // 32 bytes at once, a whole sector: lanes write rows far apart
@@ -1258,13 +1242,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               for (int i = 0; i < 8; ++i) x[i] = fma2(pair(s[2 * (i0 + i)], s[2 * (i0 + i) + 1]), scale2, base2);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                float2 e;
-                if (i < kPolyOf8) {
-                  e = exp2_poly(x[i]);
-                } else {
-                  e = split(x[i]);
-                  e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-                }
+                float2 e = split(x[i]);
+                e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
                 sums[i & 3] = add2(sums[i & 3], pair(e.x, e.y));
                 s[i0 + i] = Mma<T>::pack(e.x, e.y);
               }

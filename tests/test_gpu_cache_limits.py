@@ -69,6 +69,12 @@ class Sequences:
         tol = orc.attend_tolerance(out, reach, size, HALF_STEP[self.dtype], self.width)
         assert (np.abs(_np(got) - out) <= tol).all()
 
+    def check_token(self, got, q, t, seen):
+        """Token t of slot 0's, which sees its first `seen` rows."""
+        one = Sequences.__new__(Sequences)
+        one.rows, one.dtype, one.width = [{0: r[0][:, :seen]} for r in self.rows], self.dtype, self.width
+        one.check(got[t: t + 1], q[t: t + 1], [0], [0, 1])
+
 
 # ------------------------------------------------------------------ page copies
 @pytest.mark.parametrize("planes", [1, 2, 3])
@@ -165,8 +171,17 @@ def test_a_long_prompt_said_to_be_short(cm, most_q):
     q = _randn((2002, 4, 64), torch.float16, 6)
     got = s.cache.attend(q, _ints([0, 1, 2]), _ints([0, 2000, 2001, 2002]), prefix=-1, most_q=most_q)
     for t in (0, 1, 15, 16, 500, 1998, 1999):
-        one = Sequences.__new__(Sequences)
-        one.rows = [{0: r[0][:, : 1000 + t + 1]} for r in s.rows]
-        one.dtype, one.width = s.dtype, s.width
-        one.check(got[t: t + 1], q[t: t + 1], [0], [0, 1])
+        s.check_token(got, q, t, 1000 + t + 1)
     s.check(got[2000:], q[2000:], [1, 2], [0, 1, 2])
+
+
+@pytest.mark.parametrize("most_q", [1, 200])
+def test_values_not_seen_weigh_nothing(cm, most_q):
+    """Later tokens with V of 2^126: a weight of 2^-126 in their masked places would add 1 each."""
+    s = Sequences(cm, [200], 1, 64, 32, torch.bfloat16, seed=8)
+    for r in range(150, 200):
+        s.cache.planes[1][int(s.cache.table[0, r // 32]), :, r % 32] = 2.0 ** 126
+    q = _randn((200, 4, 64), torch.bfloat16, 9)
+    got = s.cache.attend(q, _ints([0]), _ints([0, 200]), most_q=most_q)
+    for t in (0, 1, 17, 127, 128, 149):
+        s.check_token(got, q, t, t + 1)
