@@ -147,9 +147,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowAr
     long long w = 0;
     if (J.src.paged || J.dst.paged) {
       w = a.where[t];
-      if (w < 0) return;
-      if (w >= a.n_rows) {
-        atomicOr(&g_status, kStatusIndex);
+      if (w < 0 || w >= a.n_rows) {
+        if (w != -1) atomicOr(&g_status, kStatusIndex);
         return;
       }
     }

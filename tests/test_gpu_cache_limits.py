@@ -95,6 +95,24 @@ def test_a_bad_page_among_many_copies_is_reported(cm, status, planes, at):
     assert all(torch.equal(p, w) for p, w in zip(c.planes, want))
 
 
+# ------------------------------------------------------------------ rows
+@pytest.mark.parametrize("bad", [-2, -(1 << 40), 16])
+def test_rows_before_and_behind_the_cache_are_reported(cm, status, bad):
+    """Only -1 means no row; any other number outside is an error, of rows written and of rows read."""
+    c = _cache(cm, 2, 8, 1, 2, [(1, 16)])
+    before = c.planes[0].clone()
+    rows, where = _randn((3, 16), torch.float16, 1), torch.tensor([-1, 3, bad], device="cuda")
+    c.write([0], [rows], where)
+    assert status() == orc.INDEX
+    before[0, 0, 3] = rows[1]
+    assert torch.equal(c.planes[0], before)
+    back = c.read([0], where, outs=[torch.full((3, 1, 16), 7.0, dtype=torch.float16, device="cuda")])[0]
+    assert status() == orc.INDEX
+    assert torch.equal(back[1, 0], rows[1]) and (back[[0, 2]] == 7).all()
+    c.write([0], [rows[:2]], where[:2])
+    assert status() == 0
+
+
 # ------------------------------------------------------------------ too few pages
 def _same(c, m):
     for name in ("table", "length", "refs"):
