@@ -475,7 +475,9 @@ lb_status littlebit_cache_read(const lb_cache* c, const int* planes, const lb_ro
  * Slot children[i] becomes a copy of slot parents[i]: it shares the parent's
  * full pages (refs + 1) and gets a page of its own for a partly filled last
  * one, into which the rows held are copied, in every plane.  Children must be
- * empty.  A parent may be named many times.  work_dev:
+ * empty.  A parent whose last, partly filled page is a number outside the cache
+ * is refused; such a number among its full pages is handed on and reported.
+ * A parent may be named many times.  work_dev:
  * littlebit_cache_fork_work(n) bytes, 16-byte aligned.  Two launches (one more
  * for every further 64 planes).
  */

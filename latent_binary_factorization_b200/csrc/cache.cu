@@ -573,13 +573,14 @@ __global__ void __launch_bounds__(kBookThreads, 1)
   int* s_len = sm;            // [n] tokens of the parent; -1: left out
   int* s_off = s_len + n;     // [n]
   int* s_child = s_off + n;   // [n]
+  int* s_last = s_child + n;  // [n] the parent's partly filled last page
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
   lb::dependent_begin();
   unsigned bad = 0;
   for (int i = tid; i < n; i += kBookThreads) {
     const int p = parents[i], ch = children[i];
-    int len = -1;
+    int len = -1, last = -1;
     if (p == -1 || ch == -1) {
       ;   // padding
     } else if (p < 0 || p >= c.n_slots || ch < 0 || ch >= c.n_slots || p == ch) {
@@ -587,12 +588,15 @@ __global__ void __launch_bounds__(kBookThreads, 1)
     } else {
       len = c.length[p];
       const bool lost = len < 0 || pages_of(len, c) > c.max_pages;
-      if (lost || c.length[ch] != 0) {
+      if (!lost && (len & (c.page_size - 1))) last = c.table[p * c.table_stride + (len >> c.page_shift)];
+      const bool outside = last < 0 ? len & (c.page_size - 1) : last >= c.n_pages;
+      if (lost || c.length[ch] != 0 || outside) {
         len = -1;
         bad |= kStatusIndex;
       }
     }
     s_len[i] = len;
+    s_last[i] = last;
     s_child[i] = ch;
     copy[i] = CopyJob{-1, -1, 0, 0};
   }
@@ -612,11 +616,9 @@ __global__ void __launch_bounds__(kBookThreads, 1)
   const int found = take_free(c.refs, c.n_pages, want, warp_sums, [&](int rank, int page) {
     const int i = owner_of(s_off, n, rank);
     const int full = s_len[i] >> c.page_shift;
-    const int src = c.table[parents[i] * c.table_stride + full];
     c.refs[page] = 1;
     c.table[s_child[i] * c.table_stride + full] = page;
-    if (src >= 0 && src < c.n_pages) copy[i] = CopyJob{src, page, s_len[i] & (c.page_size - 1), 0};
-    else atomicOr(&g_status, kStatusIndex);
+    copy[i] = CopyJob{s_last[i], page, s_len[i] & (c.page_size - 1), 0};
   });
   __syncthreads();
   for (int i = tid; i < n; i += kBookThreads) {
@@ -1100,9 +1102,9 @@ lb_status littlebit_cache_fork(const lb_cache* c, const int32_t* parents, const 
   CopyJob* copy = reinterpret_cast<CopyJob*>(fork + n);
   static lb::PerDevice smem;
   cudaError_t e = lb::touch_cache_status(nullptr);
-  if (e == cudaSuccess) e = allow_smem(fork_kernel, smem, 3 * kMaxList * (int)sizeof(int));
+  if (e == cudaSuccess) e = allow_smem(fork_kernel, smem, 4 * kMaxList * (int)sizeof(int));
   if (e != cudaSuccess) return lb::cuda_fail(e);
-  r = launched(lb::launch_dependent_on(st, fork_kernel, dim3(1), kBookThreads, 3 * n * sizeof(int), tables_of(*c),
+  r = launched(lb::launch_dependent_on(st, fork_kernel, dim3(1), kBookThreads, 4 * n * sizeof(int), tables_of(*c),
                                        parents, children, n, fork, copy));
   if (r != LB_OK) return r;
   for (int b = 0; b < c->n_planes; b += kPlaneBatch) {

@@ -136,9 +136,12 @@ class Model:
             if not (0 <= p < self.n_slots and 0 <= c < self.n_slots) or p == c or before[c] or c in taken:
                 self.status |= INDEX
                 continue
-            taken.add(c)
             n = int(before[p])
             full, rest = n // self.ps, n % self.ps
+            if rest and not 0 <= self.table[p, full] < self.n_pages:
+                self.status |= INDEX
+                continue
+            taken.add(c)
             if rest:
                 asked += 1
                 if asked > len(free):

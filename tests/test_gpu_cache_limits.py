@@ -157,6 +157,22 @@ def test_shortages_follow_the_model(cm, status, n_pages, n_slots, most):
     assert short   # some step took the last page
 
 
+@pytest.mark.parametrize("bad", [-1, -7, 12, 1 << 30])
+def test_a_fork_of_a_lost_last_page_is_refused(cm, status, bad):
+    """A parent whose partly filled page is a number outside the cache: no child of rows that nobody wrote, and the
+    slot stays free for another parent of the same call."""
+    c = _cache(cm, 12, 8, 5, 3, [(1, 8)])
+    m = orc.Model(12, 8, 5, 3, [c.planes[0].cpu().numpy().copy()])
+    for t, f in ((c, _ints), (m, list)):
+        t.extend(f([0, 1]), f([0, 13, 24]), 24)
+        t.table[0, 1] = bad
+        t.fork(f([0, 0, 1, 1]), f([2, 3, 2, 4]))
+    assert status() == orc.INDEX == m.status
+    _same(c, m)
+    assert c.length.tolist() == [13, 11, 11, 0, 11]
+    assert np.array_equal(c.planes[0].cpu().numpy(), m.planes[0])
+
+
 # ------------------------------------------------------------------ attention
 @pytest.mark.parametrize("most_q", [None, 1, 2, 40, 1000])
 @pytest.mark.parametrize("new,heads_q,heads", [([40, 130, 1], 4, 2), ([40, 130, 1], 8, 1), ([1, 1, 33, 1, 1, 1], 16, 2),
