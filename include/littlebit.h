@@ -536,8 +536,8 @@ lb_status littlebit_cache_copy(const lb_cache* c, const int32_t* src_dev, const 
  * and raises LB_ERR_INDEX; a slot outside it has no tokens and raises it too.
  * work_dev: littlebit_cache_attend_work bytes, 256-byte aligned, needed until
  * the call's launches are done; calls that may overlap need their own.
- * Errors: LB_ERR_ARG, LB_ERR_SHAPE, LB_ERR_ALIGN, LB_ERR_UNSUPPORTED (dtype
- * or width), LB_ERR_CUDA.
+ * Errors: LB_ERR_ARG (also a scale that is not below 2.3e38 in magnitude),
+ * LB_ERR_SHAPE, LB_ERR_ALIGN, LB_ERR_UNSUPPORTED (dtype or width), LB_ERR_CUDA.
  */
 size_t littlebit_cache_attend_work(const lb_cache* c, int k, int heads_q, int n_tokens, int n, int most_q,
                                    int with_prefix);

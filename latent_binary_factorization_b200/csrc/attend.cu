@@ -1619,7 +1619,8 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   if (V.heads != K.heads || V.width != K.width || q->width != K.width) return LB_ERR_SHAPE;
   if (out->heads != q->heads || out->width != q->width) return LB_ERR_SHAPE;
   if ((r = lb::check_token_rows(q, K.dt)) != LB_OK || (r = lb::check_token_rows(out, K.dt)) != LB_OK) return r;
-  if (!(scale == scale) || std::isinf(scale)) return LB_ERR_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;   // scores are taken in units of log 2
+  if (!std::isfinite(scale_log2)) return LB_ERR_ARG;
   if (n_tokens == 0) return LB_OK;
   if (!work) return LB_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(work) % 256) return LB_ERR_ALIGN;
@@ -1654,7 +1655,7 @@ lb_status littlebit_cache_attend(const lb_cache* c, int k, int v, const lb_rows*
   a.heads = K.heads;
   a.group = group;
   a.by_group = lb::divisor(group);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.status = status;
   JoinArgs j{};
   auto place = [&](const Region& g, unsigned char* w, bool own, bool with_prefix) {

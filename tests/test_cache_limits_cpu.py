@@ -1,5 +1,6 @@
 """The paged cache without a GPU: what its kernels' sources and numbers have to
 hold, and refusals at the ends of the ranges."""
+import ctypes
 import os
 import re
 
@@ -62,3 +63,32 @@ def test_oracle_a_refused_sequence_asks_for_nothing():
     where, _ = m.extend([0, 1, 2], [0, 80, 88, 93], 93)
     assert m.status == orc.PAGES and m.length.tolist() == [0, 8, 5]
     assert where[80:].tolist() == [*range(8), *range(8, 13)] and (where[:80] == -1).all()
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf"), 2.4e38, -3.4e38])
+def test_scales_that_overflow_are_refused(scale):
+    """Scores are in units of log 2: a finite scale times log2 e may not be."""
+    lib = ctypes.CDLL(build_ext.build())
+
+    class Plane(ctypes.Structure):
+        _fields_ = [("data", ctypes.c_void_p), ("strides", ctypes.c_int64 * 3), ("heads", ctypes.c_int),
+                    ("width", ctypes.c_int), ("dt", ctypes.c_int)]
+
+    class Cache(ctypes.Structure):
+        _fields_ = [("planes", ctypes.POINTER(Plane)), ("n", ctypes.c_int * 5), ("table_stride", ctypes.c_int64),
+                    ("arrays", ctypes.c_void_p * 3)]
+
+    class Rows(ctypes.Structure):
+        _fields_ = [("data", ctypes.c_void_p), ("strides", ctypes.c_int64 * 2), ("heads", ctypes.c_int), ("width", ctypes.c_int)]
+
+    plane = Plane(4096, (16 * 64, 16 * 64, 64), 1, 64, 0)
+    c = Cache(ctypes.pointer(plane), (1, 4, 16, 2, 2), 2, (256, 512, 768))
+    q = Rows(8192, (64, 64), 1, 64)
+    f = lib.littlebit_cache_attend
+    f.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                  ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                  ctypes.c_void_p]
+    args = [ctypes.byref(c), 0, 0, ctypes.byref(q), 1, 16, 16, 1, -1, 1]
+    assert f(*args, scale, ctypes.byref(q), 256, 1 << 40, None) == 1    # LB_ERR_ARG
+    assert f(*args, 2.3e38, ctypes.byref(q), None, 0, None) == 1        # the largest go on to the next refusal: no work memory
+    assert f(*args, 2.3e38, ctypes.byref(q), 256, 0, None) == 3         # LB_ERR_SHAPE: too little of it
