@@ -355,7 +355,8 @@ lb_status littlebit_linear_forward_noalloc(const lb_layer* layer, const void* x_
  * takes nothing from what follows it in the list, and raises a bit in the cache status word of the device, which
  * littlebit_device_status returns: LB_ERR_PAGES, no free page or no room in
  * max_pages; LB_ERR_INDEX, a slot, page or row number outside the cache, a
- * slot twice in one list, a fork into a slot that holds tokens.  A slot number
+ * slot twice in one list, a fork into a slot that holds tokens, starts that
+ * descend or lie outside the step's tokens (they are cut to what there is).  A slot number
  * of -1 in a list is padding and skipped.  Lists take up to 4096 entries.
  * Calls that change one cache, and those that read it beside them, must be
  * ordered by the caller.  Alignment: every

@@ -207,7 +207,10 @@ __device__ __forceinline__ Begin plan_block(const AttendArgs& a) {
       mine_s = stored_rows<C>(rows) * a.heads;
       head = own_head<C>(a.by_group, rows, s.len, s.before);
       mine = (long long)head * a.heads;
-      if (leave && s.slot != -1 && (s.slot < 0 || s.slot >= a.n_slots)) atomicOr(a.status, kStatusIndex);
+      if (leave) {
+        const int from = a.starts[i], to = a.starts[i + 1];
+        if (s.slot < -1 || s.slot >= a.n_slots || from < 0 || to < from || to > a.n_tokens) atomicOr(a.status, kStatusIndex);
+      }
     }
     long long xu = mine;
     int xs = mine_s;
@@ -1335,23 +1338,28 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   constexpr int E = D / 32;
   const int t = blockIdx.x, lane = threadIdx.x & 31;
   __shared__ SeqPlan s_plan;
-  __shared__ int s_found;
-  if (threadIdx.x == 0) s_found = 0;
+  __shared__ int s_found;   // the token's sequence: the last one that has it, if starts descend and several do
+  if (threadIdx.x == 0) s_found = -1;
   __syncthreads();
   lb::dependent_begin();
   PlanHead head[2];
   head[0] = *a.set[0].head;
   head[1] = a.set[1].head ? *a.set[1].head : PlanHead{1, 0, 0, 0, 0, 0, 0, 0};
+  int mine = -1;
+  SeqPlan has{};
 #pragma unroll 1
   for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
     const SeqPlan s = a.set[0].seqs[i];
     if (t >= s.first && t < s.first + s.count) {
-      s_plan = s;
-      s_found = 1;
+      has = s;
+      mine = i;
     }
   }
+  if (mine >= 0) atomicMax(&s_found, mine);
   __syncthreads();
-  if (!s_found || head[0].width == 0 || head[1].width == 0) return;
+  if (mine >= 0 && mine == s_found) s_plan = has;
+  __syncthreads();
+  if (s_found < 0 || head[0].width == 0 || head[1].width == 0) return;
   const SeqPlan s = s_plan;
 #pragma unroll 1
   for (int h = blockIdx.y * 8 + (threadIdx.x >> 5); h < a.heads * a.group; h += 8 * gridDim.y) {
@@ -1372,6 +1380,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
       int row, left, r, ua, ext, before;   // before: stored rows before the head's
       if (w) {
         row = (t - head[1].t0) * a.group + sub;
+        if ((unsigned)row >= (unsigned)head[1].p_rows) continue;   // starts descend
         r = few ? row / FewCut::kRows : row / ManyCut::kRows;
         left = head[1].p_rows - r * tile;
         ua = kv * head[1].p_head + r * extent_of(head[1].p_kt, tile);

@@ -446,6 +446,8 @@ __global__ void __launch_bounds__(256)
                   int* positions) {
   lb::dependent_begin();
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
+  for (int i = t; i < n; i += gridDim.x * blockDim.x)
+    if (starts[i] < 0 || starts[i + 1] < starts[i] || starts[i + 1] > n_tokens) atomicOr(&g_status, kStatusIndex);
   if (t >= n_tokens) return;
   int first;
   const int i = sequence_of(starts, n, n_tokens, t, first);

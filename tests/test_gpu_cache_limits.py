@@ -219,3 +219,23 @@ def test_values_not_seen_weigh_nothing(cm, most_q):
     got = s.cache.attend(q, _ints([0]), _ints([0, 200]), most_q=most_q)
     for t in (0, 1, 17, 127, 128, 149):
         s.check_token(got, q, t, t + 1)
+
+
+@pytest.mark.parametrize("most_q", [1, 60])
+@pytest.mark.parametrize("starts", [[0, 30, 10, 60], [0, 60, 0, 60], [9, 0, 12, 60], [-5, 20, 40, 60], [0, 20, 40, 61],
+                                    [60, 0, 60, 0]])
+def test_starts_that_descend_are_reported(cm, status, starts, most_q):
+    """Lists that no step has: reported by attention and by locate, nothing is written outside the outputs."""
+    s = Sequences(cm, [70, 80, 90, 300], 2, 64, 16, torch.float16, seed=10)
+    q = _randn((60, 8, 64), torch.float16, 11)
+    room = torch.full((70, 8, 64), 7.0, dtype=torch.float16, device="cuda")
+    for _ in range(3):
+        s.cache.attend(q, _ints([0, 1, 2]), _ints(starts), prefix=3, most_q=most_q, out=room[5:65])
+    assert status() == orc.INDEX
+    assert (room[:5] == 7).all() and (room[65:] == 7).all()
+    s.cache.locate(_ints([0, 1, 2]), _ints(starts), 60)
+    assert status() == orc.INDEX
+    out = torch.full_like(q, 7.0)
+    s.cache.attend(q, _ints([0, 1, 2]), _ints([0, 20, 40, 60]), prefix=3, most_q=most_q, out=out)   # and the next call is right
+    s.check(out, q, [0, 1, 2], [0, 20, 40, 60], 3)
+    assert status() == 0
