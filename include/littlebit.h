@@ -522,9 +522,9 @@ lb_status littlebit_cache_copy(const lb_cache* c, const int32_t* src_dev, const 
  * 128); q and out have their dtype, q.heads a multiple of the planes' heads:
  * query head h reads head h / (q.heads / heads).  most_q (1 at least): the
  * tokens of the longest sequence as far as the caller knows them; it decides
- * which kernel takes the sequences' own keys (up to 32 rows of tokens x query
- * heads of one K and V head: the one for few rows).  Sequences longer or
- * shorter than that come out the same but for rounding.
+ * which kernel takes the sequences' own keys (up to 16 rows of tokens x query
+ * heads of one K and V head, 32 in small batches: the one for few rows).
+ * Sequences longer or shorter than that come out the same but for rounding.
  * The prefix is read and multiplied once for the whole batch.  Scores, sums
  * and outputs are accumulated in fp32; the weights are rounded to the dtype
  * for the product with V, the outputs once at the end.  Rows past a

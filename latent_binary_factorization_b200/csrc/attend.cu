@@ -1494,16 +1494,18 @@ Region region(int tile, int blocks, int64_t rows, int n, int D) {
 }
 
 // Which launch takes what: the rows that read a key set decide.  A sequence's
-// own keys go to the few-rows kernel up to two tiles of it (64 sequences of up
-// to 1000 keys, 8 heads of 128: 24 rows 47 us there, 57 in the many-rows kernel;
-// 32 rows 60 and 60; 64 rows 99 and 67).  The prefix goes there only if one tile
-// holds its rows: two read it twice (32 rows over 64000 keys: 106 us and 68),
-// though over a short one that costs less than the other kernel's beginning
-// (8192 keys: 28 and 32); how long it is, is known on the device alone.  So are the
-// tokens of each sequence: most_q decides by what the caller knows, and either
-// kernel takes any number, so the work memory has room for any division of the
-// batch's tokens.
-constexpr int kFewPrefix = kFewRows, kFewOwn = 2 * kFewRows;
+// own keys go to the few-rows kernel if one tile of it holds its rows: 0.65 to
+// 0.97 of the many-rows kernel's time for 4 to 64 sequences of 100 to 8000 keys,
+// 2 and 8 heads of 128 (16 rows).  Two tiles read the keys twice, which only a
+// batch with little to read takes lightly: 24 and 32 rows, up to 32 sequences x
+// heads, 0.66 to 0.97 (1.2 at 4000 to 8000 keys); 128 and 512 of them, 0.98 to
+// 1.5.  The prefix goes there only if one tile holds its rows (32 rows over 64000
+// keys: 103 us and 63), though over a short one two cost less than the other
+// kernel's beginning (2000 keys: 15 and 20; 8192: 25 and 25); how long it is, is
+// known on the device alone.  So are the tokens of each sequence: most_q decides
+// by what the caller knows, and either kernel takes any number, so the work
+// memory has room for any division of the batch's tokens.
+constexpr int kFewSegments = 32;   // sequences x heads of a batch with little to read
 struct Split {
   bool few_prefix, few_own, many_prefix, many_own;
   Region few, many;
@@ -1511,9 +1513,9 @@ struct Split {
 Split split_of(int heads, int group, int n_tokens, int n, int most_q, bool with_prefix, int D) {
   Split s{};
   const int64_t p_rows = (int64_t)n_tokens * group, o_rows = (int64_t)most_q * group;
-  s.few_prefix = with_prefix && p_rows <= kFewPrefix;
+  s.few_prefix = with_prefix && p_rows <= kFewRows;
   s.many_prefix = with_prefix && !s.few_prefix;
-  s.few_own = o_rows <= kFewOwn;
+  s.few_own = o_rows <= ((int64_t)n * heads <= kFewSegments ? 2 * kFewRows : kFewRows);
   s.many_own = !s.few_own;
   // Stored rows at most: one for each query row, and in the many-rows kernel 128 more for a narrow last tile, which
   // the prefix and every sequence may have.
