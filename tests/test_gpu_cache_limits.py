@@ -239,3 +239,36 @@ def test_starts_that_descend_are_reported(cm, status, starts, most_q):
     s.cache.attend(q, _ints([0, 1, 2]), _ints([0, 20, 40, 60]), prefix=3, most_q=most_q, out=out)   # and the next call is right
     s.check(out, q, [0, 1, 2], [0, 20, 40, 60], 3)
     assert status() == 0
+
+
+# ------------------------------------------------------------------ together
+def test_attention_over_a_cache_of_latent_rows(cm, status):
+    """K and V projections kept as latent rows in one paged cache: located, read, expanded, rotated into a second cache
+    of K and V heads and attended there; the expanded rows are those of the projections' own latents."""
+    from latent_binary_factorization_b200 import layers, littlebit as lb, synth
+    d, heads, width, n = 256, 4, 64, 48
+    kv = [layers.upload(synth.layer(d, heads * width, 48, False, seed=i), d, heads * width, 48) for i in (1, 2)]
+    latent = cm.Cache.empty([(1, lb.latent_row_elems(x)) for x in kv], 8, 16, 2, 4)
+    x = torch.randn((n, d), generator=torch.Generator().manual_seed(2)).half().cuda()
+    parts = [lb.latent_forward(kv, [x[a: a + 16]] * 2) for a in range(0, n, 16)]
+    slot, rope = _ints([1]), cm.Rotary(width)
+    for p in parts:                                           # as three steps of 16 tokens bring them
+        where, _ = latent.extend(slot, _ints([0, 16]), 16)
+        latent.write([0, 1], list(p), where)
+    heads_cache = cm.Cache.empty([(heads, width)] * 2, 4, 16, 1, 4)
+    for a, p in zip(range(0, n, 16), parts):
+        at, positions = latent.locate(slot, _ints([0, 16]), 16, first=_ints([a]))
+        rows = latent.read([0, 1], at)
+        for r, t, layer in zip(rows, p, kv):
+            assert torch.equal(r[:, 0, : layer.s], t[:, : layer.s])
+        k, v = lb.latent_expand(kv, [r[:, 0].contiguous() for r in rows])
+        where, _ = heads_cache.extend(_ints([0]), _ints([0, 16]), 16)
+        heads_cache.write([0, 1], [y.view(16, heads, width) for y in (k, v)], where, rope=rope, positions=positions, rotated=[0])
+    q = _randn((3, 8, width), torch.float16, 3)
+    q = cm.rotate([q], _ints(range(n - 3, n)), rope)[0]
+    out = heads_cache.attend(q, _ints([0]), _ints([0, 3]))
+    at, _ = heads_cache.locate(_ints([0]), _ints([0, n]), n)
+    k, v = (_np(r).transpose(1, 0, 2) for r in heads_cache.read([0, 1], at))
+    want, reach, size = orc.attend(_np(q), lambda s: k, lambda s: v, [0], [0, 3])
+    assert (np.abs(_np(out) - want) <= orc.attend_tolerance(want, reach, size, 2.0 ** -11, width)).all()
+    assert status() == 0
