@@ -527,14 +527,18 @@ lb_status littlebit_cache_copy(const lb_cache* c, const int32_t* src_dev, const 
  * Sequences longer or shorter than that come out the same but for rounding.
  * The prefix is read and multiplied once for the whole batch.  Scores, sums
  * and outputs are accumulated in fp32; the weights are rounded to the dtype
- * for the product with V, the outputs once at the end.  Rows past a
+ * for the product with V (half a step of each; of fp16's smallest at most 2^-25
+ * of the row's largest), the outputs once at the end.  Rows past a
  * sequence's end are never used, whatever they hold.  (A non-finite V of a
  * token may reach the outputs of earlier tokens of the same call and
  * sequence, whose weight for it is zero.)
  * Two or three launches.  Limits: n_tokens * q.heads <= 2^22, max_pages *
  * page_size <= 2^24 tokens; the planes' strides must be positive multiples of 16
  * bytes below 2^40.  A page number outside the cache counts as a page of zeros
- * and raises LB_ERR_INDEX; a slot outside it has no tokens and raises it too.
+ * and raises LB_ERR_INDEX; a slot outside it has no tokens and raises it too,
+ * and so has -1, without a report: such rows see the prefix alone.  A call of
+ * more work than 2^31 key tiles (of 128 query rows x 128 keys, or 16 x 64) does
+ * nothing and raises LB_ERR_INDEX.
  * work_dev: littlebit_cache_attend_work bytes, 256-byte aligned, needed until
  * the call's launches are done; calls that may overlap need their own.
  * Errors: LB_ERR_ARG (also a scale that is not below 2.3e38 in magnitude),

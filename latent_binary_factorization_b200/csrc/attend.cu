@@ -37,10 +37,11 @@ constexpr unsigned kStatusIndex = 1u << LB_ERR_INDEX;
 
 // How a kernel cuts its segments: query rows of a tile, keys of a tile, units
 // that a segment's beginning and end are worth, units of one key tile.  A wide
-// row tile, of more than 128 rows, costs two (see many_rows_kernel).  kSetup is
-// measured: with 3, 5, 6, 9 and 12 a batch of pieces of prompts (16 sequences of
-// up to 130 tokens over a prefix of 12000, each with own keys) took 727, 560,
-// 551, 557 and 566 us, as its short segments end late or early.
+// row tile, of more than 128 rows, costs two (see many_rows_kernel).  ManyCut's
+// kSetup is measured: with 3, 5, 6 and 9 a batch of pieces of prompts (16 sequences
+// of up to 130 tokens over a prefix of 12000, each with own keys) takes 671, 596,
+// 592 and 594 us, as its short segments end late or early, and one of 48 single
+// tokens over a prefix of 8192 61.4, 62.0, 61.6 and 61.9.
 // `stored`: rows of a partial of a segment whose query rows end `left` from its
 // first: those of a narrow tile of many_rows_kernel come in two ways, 128 apart.
 struct FewCut {
@@ -412,8 +413,10 @@ struct Piece {
 // mma.sync is enough here: a tile's two products take about 600 cycles of the
 // 1400 in which HBM delivers it to an SM.  The four partials are joined through
 // shared memory when a segment ends.  Measured: 8 sequences of up to 4000 tokens
-// over a prefix of 32000, 32 heads of 128, fp16: 135 us with the join, 5.9 TB/s,
-// 91 % of the copy rate; every byte of K and V is read once.
+// over a prefix of 32000, 32 heads of 128, fp16, with the join: 135 us, 5.9 TB/s,
+// 91 % of the copy rate, in bursts of a few ms at 1965 MHz; 147 us, 5.5 TB/s, in
+// runs of seconds, which the power cap holds at 1.8 GHz.  Every byte of K and V is
+// read once.
 constexpr int kFewRows = FewCut::kRows, kFewKeys = FewCut::kKeys, kFewThreads = 128;
 
 template <int D> constexpr int kFewStages = D == 128 ? 3 : 6;
@@ -749,13 +752,17 @@ done:
 // of them by a polynomial on the multiply-add units, exact to 2^-22.5, took 599
 // and 602 us for 594.)
 // Measured: 16 pieces of up to 130 tokens over a prefix of 12000, 64 query heads
-// on 8, bf16: 540 us with the join, 848 TFLOP/s; 4096 tokens of 32 heads over
-// 23000 keys, fp16: 853 TFLOP/s.
+// on 8, bf16, with the join: 558 us, 820 TFLOP/s, in bursts at 1965 MHz, 592 us,
+// 773 TFLOP/s, in runs of seconds under the power cap; 4096 tokens of 32 heads
+// over 23000 keys, fp16: 766 TFLOP/s in such runs.
 // The running maximum is raised, and O rescaled in tensor memory, only when a
-// tile's maximum exceeds it by more than 8 (a factor 256, which the 16-bit
-// weights and fp32 sums hold without loss of precision), i.e. hardly ever after
-// the first tiles.  V rows past the end of the keys are zeroed in shared memory
-// (0 x NaN is not 0), scores there are masked, so K may hold anything.
+// tile's maximum exceeds it by more than 8 (a factor 256, for which the 16-bit
+// weights and fp32 sums have room), i.e. hardly ever after the first tiles.  The
+// weights are rounded to the type for the product, the sum takes them before: half
+// a step each, what a 16-bit product costs, and fp16 weights below 2^-14 of their
+// part's reference are off by 2^-25 of it (a part: the keys of one chain).  V rows
+// past the end of the keys are zeroed in shared memory (0 x NaN is not 0), scores
+// there are masked, so K may hold anything.
 constexpr int kTile = 128;          // rows of a group's query tile
 constexpr int kKeys = ManyCut::kKeys;
 constexpr int kManyThreads = 384;   // two softmax groups, and four warps of which the first loads

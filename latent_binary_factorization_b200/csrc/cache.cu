@@ -114,7 +114,8 @@ struct Item {
 // thread at a time: eight blocks an SM hide the latency, and two or four items
 // a thread cost more in registers than they bring (a rotary prompt of 2048
 // tokens x 72 heads, bf16: 18.5 us with one, 19.8 with two, 33 with four).  4096
-// tokens of 64 + 8 + 8 heads written: 31 us, 5.4 TB/s, 82 % of the copy rate.
+// tokens of 64 + 8 + 8 heads written: 31 us, 5.4 TB/s, 82 % of the copy rate (33
+// in runs of seconds, under the power cap).
 template <class T>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowArgs a) {
   constexpr int E = 16 / sizeof(T);

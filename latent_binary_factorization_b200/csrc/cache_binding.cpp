@@ -1,7 +1,9 @@
 // The Python face of the paged cache's calls (cache.py): checks and marshals
 // torch tensors and calls the C entry points of littlebit.h.  A serving step
 // makes several of these calls a layer, each a few microseconds on the GPU, so
-// the marshalling is compiled: about 3 us a call against 20 in Python.
+// the marshalling is compiled: a call takes 3 (free) to 11 us (compact, three new
+// tensors) on the host with its launches, 5 rotate, 4 write, 7 attend, against 20
+// to 36 in Python.
 //
 // Every function takes what its wrapper in cache.py documents, runs on the
 // current stream of the tensors' device (which is made current for the call),

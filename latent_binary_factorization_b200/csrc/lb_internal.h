@@ -272,7 +272,8 @@ cudaError_t launch_dependent_on(cudaStream_t st, void (*kern)(P...), dim3 grid, 
 }
 #endif
 
-// Division by a number fixed at launch, exact for 0 <= n < 2^31: with 2^shift
+// Division by a number fixed at launch (Granlund and Montgomery, Division by
+// invariant integers using multiplication, 1994), exact for 0 <= n < 2^31: with 2^shift
 // >= d, (n mul / 2^32 + n) / 2^shift, mul = floor(2^32 (2^shift - d) / d) + 1.
 struct Divisor {
   unsigned mul, shift;
