@@ -311,8 +311,8 @@ __device__ __forceinline__ int claim_value(int n, int i) { return -(n - i); }
 // ------------------------------------------------------------------ extend
 
 __global__ void __launch_bounds__(kBookThreads, 1)
-    extend_kernel(const Tables c, const int* slots, const int* starts, int n, int n_tokens,
-                  int prefix, long long* where, int* positions) {
+    extend_kernel(const Tables c, const int* slots, const int* starts, int n, int n_tokens, int prefix, long long* where,
+                  int* positions) {
   extern __shared__ int sm[];
   int* s_start = sm;              // [n + 1]
   int* s_len = s_start + n + 1;   // [n] tokens before the call; -1: not extended
@@ -399,8 +399,7 @@ __global__ void __launch_bounds__(kBookThreads, 1)
     }
     __syncthreads();
     for (int i = tid; i < n; i += kBookThreads)
-      s_off[i] = s_len[i] < 0 ? 0
-                              : (int)(((long long)s_len[i] + count(i) + c.page_size - 1) >> c.page_shift) - pages_of(s_len[i], c);
+      s_off[i] = s_len[i] < 0 ? 0 : pages_of(s_len[i] + count(i), c) - pages_of(s_len[i], c);
     __syncthreads();
     if (tid == 0) {
       int left = found;
@@ -442,9 +441,8 @@ __global__ void __launch_bounds__(kBookThreads, 1)
 }
 
 __global__ void __launch_bounds__(256)
-    locate_kernel(const Tables c, const int* slots, const int* starts,
-                  const int* begin, int n, int n_tokens, int prefix, long long* where,
-                  int* positions) {
+    locate_kernel(const Tables c, const int* slots, const int* starts, const int* begin, int n, int n_tokens, int prefix,
+                  long long* where, int* positions) {
   lb::dependent_begin();
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
   for (int i = t; i < n; i += gridDim.x * blockDim.x)
@@ -570,8 +568,7 @@ struct ForkJob {
 };
 
 __global__ void __launch_bounds__(kBookThreads, 1)
-    fork_kernel(const Tables c, const int* parents, const int* children, int n,
-                ForkJob* fork, CopyJob* copy) {
+    fork_kernel(const Tables c, const int* parents, const int* children, int n, ForkJob* fork, CopyJob* copy) {
   extern __shared__ int sm[];
   int* s_len = sm;            // [n] tokens of the parent; -1: left out
   int* s_off = s_len + n;     // [n]
@@ -643,8 +640,8 @@ __global__ void __launch_bounds__(kBookThreads, 1)
 
 // Blocks y = 0 first share out the children's table rows, then all copy the last pages.
 __global__ void __launch_bounds__(256)
-    fork_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, const ForkJob* fork,
-                     const CopyJob* copy, int n, int with_tables) {
+    fork_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, const ForkJob* fork, const CopyJob* copy, int n,
+                     int with_tables) {
   lb::dependent_begin();
   if (with_tables && blockIdx.y == 0)
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
@@ -664,8 +661,7 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ compact
 
 __global__ void __launch_bounds__(kBookThreads, 1)
-    compact_kernel(const Tables c, int* refs_out, int* count_out, CopyJob* jobs,
-                   int* moved, int* n_jobs) {
+    compact_kernel(const Tables c, int* refs_out, int* count_out, CopyJob* jobs, int* moved, int* n_jobs) {
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
   lb::dependent_begin();
@@ -720,9 +716,8 @@ __global__ void __launch_bounds__(kBookThreads, 1)
 }
 
 __global__ void __launch_bounds__(256)
-    compact_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, int* table_out,
-                        const int* count, const CopyJob* jobs,
-                        const int* moved, const int* n_jobs, int with_tables) {
+    compact_copy_kernel(const __grid_constant__ CopyArgs a, const Tables c, int* table_out, const int* count,
+                        const CopyJob* jobs, const int* moved, const int* n_jobs, int with_tables) {
   lb::dependent_begin();
   if (with_tables) {
     const int live = *count;
@@ -738,8 +733,7 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(256)
-    copy_kernel(const __grid_constant__ CopyArgs a, const int* src, const int* dst, int n,
-                int n_pages) {
+    copy_kernel(const __grid_constant__ CopyArgs a, const int* src, const int* dst, int n, int n_pages) {
   lb::dependent_begin();
   copy_items(a, n, [&](int i) {
     CopyJob j{src[i], dst[i], a.page_size, 0};
